@@ -682,3 +682,10 @@ def recurrent_kda(q, k, v, gate, beta, initial_state=None, *, cu_seqlens=None,
     else:
         kda_recurrent_fwd(q, k, v, g, beta, h0, cu, shape, o, ht, dev_status, stream)
     return o, ht
+
+
+# The recurrent block's other operators (their functions and constants join this module's).
+from . import block as _block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += _block.__all__

@@ -30,6 +30,10 @@ SOURCES = [
     "kda_chunk_bwd.cu",
     "kda_profile.cu",
     "kda_noalloc.cu",
+    "kda_block_api.cu",
+    "kda_conv.cu",
+    "kda_norm.cu",
+    "kda_ssm.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

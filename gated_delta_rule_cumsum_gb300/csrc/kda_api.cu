@@ -692,6 +692,8 @@ kda_status kda_read_device_status(const int32_t *dev_status, int32_t *host_bits,
     if (bits & KDA_DEVICE_GATE_RANGE)
         return fail(KDA_ERR_UNSUPPORTED, "kda_chunk_bwd: a chunk's gate range exceeds what the "
                     "chunked backward takes (its gradients were not computed)");
+    if (bits & KDA_DEVICE_BAD_INDEX)
+        return fail(KDA_ERR_INVALID_ARG, "device reported a state index past the last slot");
     if (bits & KDA_DEVICE_INTERNAL)
         return fail(KDA_ERR_CUDA, "a kernel found an internal launch invariant broken");
     return KDA_OK;

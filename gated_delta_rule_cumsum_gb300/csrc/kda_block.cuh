@@ -1,0 +1,186 @@
+// kda_block.cuh -- the recurrent block's operators beside KDA itself (short causal
+// convolution, selective state-space scan, residual RMS norm): their argument structs
+// and launchers, and small helpers they share.  Not part of the public ABI.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// ------------------------------------------------------------ short convolution
+struct ConvArgs {
+    const void *x, *state_in;      // [B, T, C] rows x_stride apart; [N, W-1, C]
+    const float *w, *bias;         // [C, W]; [C] or null
+    const int32_t *cu;
+    void *y, *state_out;           // forward outputs
+    const void *dy, *dstate_out;   // backward
+    void *dx, *dstate_in;
+    float *dw, *dbias;
+    float *part;                   // backward: [parts][W + 1][C] partial sums of dw and dbias
+    int32_t *status;
+    int64_t x_stride;
+    int B, T, C, W, N, silu;
+    int strip;                     // rows a thread walks
+    int64_t strips;                // over all B * T rows
+};
+// Rows per strip: chosen so that a call has enough threads to hide memory latency.
+int conv_strip(int B, int T, int C, int vec);
+int conv_bwd_strip(int B, int T, int C);
+cudaError_t launch_conv_fwd(ConvArgs a, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_conv_bwd(ConvArgs a, kda_dtype dt, cudaStream_t st);
+
+struct ConvStepArgs {
+    const void *x;
+    const float *w, *bias;
+    void *state;                   // [slots, W-1, C], updated in place
+    const int32_t *idx;            // [N] or null
+    void *y;
+    int32_t *status;
+    int64_t x_stride;
+    int N, slots, C, W, silu;
+};
+cudaError_t launch_conv_step(const ConvStepArgs &a, kda_dtype dt, cudaStream_t st);
+
+// ------------------------------------------------------------------------- norm
+struct NormArgs {
+    const void *x, *res;           // [rows, cols]; res may be null
+    const float *w;
+    void *h, *y;                   // h may be null (not stored)
+    float *scale;                  // 8-bit outputs: [rows, groups]
+    int64_t rows;
+    int cols, group, out;          // group: columns per scale (0: the row); out: kda_norm_out
+    float eps;
+    // backward
+    const void *dy, *dres;
+    void *dx;
+    float *dw, *part;
+};
+int64_t norm_bwd_parts(int64_t rows, int cols);
+cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st);
+
+// ------------------------------------------------------------------------- scan
+struct SsmArgs {
+    const void *x, *dt, *Bm, *Cm;  // rows x_stride, dt_stride, b_stride, c_stride apart
+    const float *A_log, *D, *dt_bias, *h0;
+    const int32_t *cu;
+    void *y;
+    float *ht;
+    int32_t *status;
+    int64_t x_stride, dt_stride, b_stride, c_stride;
+    int B, T, H, G, Ns, P, N, softplus;  // Ns: state rows, N: sequences
+    int L;                               // chunk length
+    // workspace
+    ChunkCtrl *ctrl;
+    int32_t *chunk_start;          // [N + 1] (packed only)
+    int64_t slots;
+    float *states;                 // [slots][H][Ns][P]: the state at each chunk's start
+    float *decay;                  // [slots][H]: each chunk's decay from start to end
+    // backward
+    const void *dy;
+    const float *dht;
+    void *dx, *ddt, *dB, *dC;
+    float *dA_log, *dD, *ddt_bias, *dh0;
+    float *dstates;                // [slots][H][Ns][P]: the state gradient at each chunk's end
+    float *dBh, *dCh;              // [rows][H][Ns]: the heads' shares of dB and dC
+    float *sums;                   // [slots][3][H]: the chunks' shares of dA_log, dD, ddt_bias
+};
+int ssm_chunk_len(kda_dtype dt, int Ns, int P);
+cudaError_t launch_ssm_fwd(const SsmArgs &a, kda_dtype dt, cudaStream_t st);
+// The chunk states alone (the first part of the forward).
+cudaError_t launch_ssm_states(const SsmArgs &a, kda_dtype dt, cudaStream_t st);
+cudaError_t launch_ssm_bwd(const SsmArgs &a, kda_dtype dt, cudaStream_t st);
+
+struct SsmStepArgs {
+    const void *x, *dt, *Bm, *Cm;
+    const float *A_log, *D, *dt_bias;
+    float *state;                  // [slots, H, Ns, P], updated in place
+    const int32_t *idx;
+    void *y;
+    int32_t *status;
+    int64_t x_stride, dt_stride, b_stride, c_stride;
+    int N, slots, H, G, Ns, P, softplus;
+};
+cudaError_t launch_ssm_step(const SsmStepArgs &a, kda_dtype dt, cudaStream_t st);
+
+// ---------------------------------------------------------------------- helpers
+// VEC consecutive elements as fp32: one vector load when the address is aligned for it
+// (ALIGNED), else scalar loads of the first `n`, zeros after.
+template <typename T, int VEC, bool ALIGNED>
+__device__ __forceinline__ void load_vec(const T *p, int n, float (&v)[VEC]) {
+    if constexpr (ALIGNED) {
+        if constexpr (sizeof(T) == 4) {
+            static_assert(VEC == 4, "fp32 vectors of four");
+            const float4 f = *reinterpret_cast<const float4 *>(p);
+            v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        } else if constexpr (VEC == 8) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __bfloat1622float2(h[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        } else {
+            static_assert(VEC == 4, "bf16 vectors of four or eight");
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 f = __bfloat1622float2(h[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+}
+
+template <typename T, int VEC, bool ALIGNED>
+__device__ __forceinline__ void store_vec(T *p, int n, const float (&v)[VEC]) {
+    if constexpr (ALIGNED) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            __nv_bfloat162 h[VEC / 2];
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(h);
+            else
+                *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(h);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < n) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+inline bool aligned_to(const void *p, size_t a) { return (uintptr_t)p % a == 0; }
+
+// The packed-offset checks of every call, by the threads of one block: the work itself
+// clamps what it reads from the offsets, so bad ones cannot lead out of bounds.
+__device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, int32_t *status) {
+    bool ok = true;
+    for (int n = threadIdx.x; n < N; n += blockDim.x)
+        ok = ok && cu[n] >= 0 && cu[n] <= cu[n + 1] && cu[n + 1] <= T;
+    if (threadIdx.x == 0) ok = ok && cu[0] == 0 && cu[N] >= 0 && cu[N] <= T;
+    if (!ok) report(status, KDA_DEVICE_BAD_CU_SEQLENS);
+}
+
+// The state slot of a batch row: its index, or the row itself without an index table.
+// Negative entries are unused rows; entries past the last slot are reported.  -1: skip.
+__device__ __forceinline__ int state_slot(const int32_t *idx, int n, int slots, int32_t *status) {
+    const int s = idx ? idx[n] : n;
+    if (s >= slots) {
+        if (threadIdx.x == 0) report(status, KDA_DEVICE_BAD_INDEX);
+        return -1;
+    }
+    return s < 0 ? -1 : s;
+}
+
+}  // namespace kda

@@ -82,11 +82,11 @@ __global__ void __launch_bounds__(128) gate_cumsum_kernel(const float *__restric
 }
 
 // Single CTA: validates cu[0..N] and, when asked, writes the chunk table
-// chunk_start[n] = sum_{m < n} ceil((cu[m+1] - cu[m]) / BT) and the control word.
+// chunk_start[n] = sum_{m < n} ceil((cu[m+1] - cu[m]) / chunk) and the control word.
 __global__ void __launch_bounds__(1024) validate_offsets_kernel(const int32_t *__restrict__ cu,
                                                                 int N, int T,
                                                                 int32_t *status, ChunkCtrl *ctrl,
-                                                                int32_t *chunk_start) {
+                                                                int32_t *chunk_start, int chunk) {
     __shared__ int32_t part[1024];
     const int tid = threadIdx.x, nt = blockDim.x;
     const int per = (N + nt - 1) / nt;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(1024) validate_offsets_kernel(const int32_t *_
     for (int n = lo; n < hi; ++n) {
         const int32_t a = cu[n], c = cu[n + 1];
         ok = ok && (a >= 0) && (a <= c) && (c <= T);
-        if (a <= c) local += (c - a + kBT - 1) / kBT;
+        if (a <= c) local += (c - a + chunk - 1) / chunk;
     }
     if (tid == 0) ok = ok && (cu[0] == 0) && (cu[N] <= T) && (cu[N] >= 0);
     const bool all_ok = __syncthreads_and(ok) != 0;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(1024) validate_offsets_kernel(const int32_t *_
         for (int n = lo; n < hi; ++n) {
             chunk_start[n] = run;
             const int32_t a = cu[n], c = cu[n + 1];
-            if (a <= c) run += (c - a + kBT - 1) / kBT;
+            if (a <= c) run += (c - a + chunk - 1) / chunk;
         }
         if (hi == N && lo <= N) chunk_start[N] = run;
         if (N == 0 && tid == 0) chunk_start[0] = 0;
@@ -136,11 +136,13 @@ __global__ void __launch_bounds__(1024) validate_offsets_kernel(const int32_t *_
 }  // namespace
 
 cudaError_t launch_validate_offsets(const int32_t *cu, int N, int T, int32_t *dev_status,
-                                    ChunkCtrl *ctrl, int32_t *chunk_start, cudaStream_t st) {
+                                    ChunkCtrl *ctrl, int32_t *chunk_start, cudaStream_t st,
+                                    int chunk) {
     int threads = 32;
     while (threads < 1024 && threads < N) threads *= 2;
     prof_begin("validate_offsets", st);
-    validate_offsets_kernel<<<1, threads, 0, st>>>(cu, N, T, dev_status, ctrl, chunk_start);
+    validate_offsets_kernel<<<1, threads, 0, st>>>(cu, N, T, dev_status, ctrl, chunk_start,
+                                               chunk);
     prof_end(st);
     return cudaGetLastError();
 }

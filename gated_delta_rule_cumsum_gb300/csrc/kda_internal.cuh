@@ -97,7 +97,8 @@ void prof_end(cudaStream_t st);
 // --------------------------------------------------------------- launchers
 // Each returns the launch error (cudaSuccess when enqueued).
 cudaError_t launch_validate_offsets(const int32_t *cu, int N, int T, int32_t *dev_status,
-                                    ChunkCtrl *ctrl, int32_t *chunk_start, cudaStream_t st);
+                                    ChunkCtrl *ctrl, int32_t *chunk_start, cudaStream_t st,
+                                    int chunk = kBT);
 
 // Input activations (kda_activation): the natural-log gate
 // -exp(A_log[hv]) softplus(g + dt_bias[hv, d]) in g's place when A_log is set,

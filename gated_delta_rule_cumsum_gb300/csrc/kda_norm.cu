@@ -1,0 +1,395 @@
+// kda_norm.cu -- a block's entry: the residual's addition and the RMS norm in one pass,
+// with the output in the input's type or in 8 bits with scales, and the gradients.
+//
+//     h = x + res,   y = h w / sqrt(mean(h^2) + eps)
+//     8 bits: scale = max |y| / top over a row (or over 128 columns of it; 1 where every
+//     y is 0), q = round(y / scale), top = 448 (e4m3) or 127 (int8)
+//
+// A row stays in its threads' registers between the sums and the output, so every input
+// is read once and every output written once: bandwidth-bound (2 flops a byte).  The sum
+// h is kept in fp32 for the norm; the stored h is rounded once, beside it.
+#include <cuda_fp8.h>
+
+#include "kda_block.cuh"
+
+namespace kda {
+namespace {
+
+// Threads that share a row: `tpr` (a multiple of 32); blockDim.x / tpr rows per block.
+// red holds one float per warp and value.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float *red) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (tpr == 32) return;
+    const int warps = tpr >> 5, warp = threadIdx.x >> 5, first = (threadIdx.x / tpr) * warps;
+    __syncthreads();  // the previous use of red is over
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[i * 32 + warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float s = 0.f;
+        for (int k = 0; k < warps; ++k) s += red[i * 32 + first + k];
+        v[i] = s;
+    }
+}
+__device__ __forceinline__ float row_max(float v, int tpr, float *red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (tpr == 32) return v;
+    const int warps = tpr >> 5, warp = threadIdx.x >> 5, first = (threadIdx.x / tpr) * warps;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    for (int k = 0; k < warps; ++k) v = fmaxf(v, red[first + k]);
+    return v;
+}
+
+// VEC 8-bit values, vector-stored when ALIGNED.
+template <int VEC, bool AL>
+__device__ __forceinline__ void store_q(uint8_t *p, int n, const float (&v)[VEC], int out) {
+    union {
+        uint8_t b[VEC];
+        uint32_t w[VEC / 4];
+    } u;
+    if (out == KDA_NORM_E4M3) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const __nv_fp8x2_storage_t f =
+                __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3);
+            u.b[i] = (uint8_t)(f & 0xff);
+            u.b[i + 1] = (uint8_t)(f >> 8);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            u.b[i] = (uint8_t)(int8_t)__float2int_rn(fminf(fmaxf(v[i], -127.f), 127.f));
+    }
+    if constexpr (AL && VEC == 8) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(u.w[0], u.w[1]);
+    } else if constexpr (AL) {
+        *reinterpret_cast<uint32_t *>(p) = u.w[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < n) p[i] = u.b[i];
+    }
+}
+
+// NV vectors of VEC columns per thread: thread i of a row holds vectors i, i + tpr, ...
+// Eight (bf16) or four (fp32) adjacent columns per thread make a 128-column scale group
+// 16 or 32 adjacent lanes of one warp.
+template <typename T, int VEC, int NV, bool AL, bool Q, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormArgs p, int tpr) {
+    __shared__ float red[32];
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const int tid = threadIdx.x % tpr;
+    const bool live = row < p.rows;
+    const T *x = static_cast<const T *>(p.x) + row * p.cols;
+    const T *res = static_cast<const T *>(p.res) + row * p.cols;
+    T *h = static_cast<T *>(p.h) + row * p.cols;
+
+    float v[NV][VEC];
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
+        if (live && n > 0) load_vec<T, VEC, AL>(x + c, n, v[i]);
+    }
+    if (p.res) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            float r[VEC];
+            if (live && n > 0) {
+                load_vec<T, VEC, AL>(res + c, n, r);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[i][j] += r[j];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+        if (live && n > 0 && p.h) store_vec<T, VEC, AL>(h + c, n, v[i]);
+    }
+    row_sum<1>(ss, tpr, red);
+    const float rstd = 1.f / sqrtf(ss[0] / (float)p.cols + p.eps);
+
+    float amax = 0.f;
+    float gmax[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+        float w[VEC] = {};
+        if (n > 0) {
+            if constexpr (AL) {
+#pragma unroll
+                for (int j = 0; j < VEC; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(p.w + c + j);
+                    w[j] = f.x; w[j + 1] = f.y; w[j + 2] = f.z; w[j + 3] = f.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) w[j] = j < n ? p.w[c + j] : 0.f;
+            }
+        }
+        gmax[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            v[i][j] = v[i][j] * rstd * w[j];
+            if (Q) gmax[i] = fmaxf(gmax[i], fabsf(v[i][j]));
+        }
+        if constexpr (!Q) {
+            if (live && n > 0)
+                store_vec<T, VEC, AL>(static_cast<T *>(p.y) + row * p.cols + c, n, v[i]);
+        } else {
+            amax = fmaxf(amax, gmax[i]);
+        }
+    }
+    if constexpr (Q) {
+        const float top = p.out == KDA_NORM_E4M3 ? 448.f : 127.f;
+        uint8_t *q = static_cast<uint8_t *>(p.y) + row * p.cols;
+        if (p.group == 0) amax = row_max(amax, tpr, red);
+        const int groups = p.group ? (p.cols + 127) / 128 : 1;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            float m = amax;
+            if (p.group) {
+                m = gmax[i];
+#pragma unroll
+                for (int o = 64 / VEC; o > 0; o >>= 1)
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            }
+            const float scale = m > 0.f ? m / top : 1.f;
+            const float inv = 1.f / scale;
+            if (live && n > 0) {
+                if (p.group ? c % 128 == 0 : c == 0)
+                    p.scale[row * groups + (p.group ? c / 128 : 0)] = scale;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[i][j] *= inv;
+                store_q<VEC, AL>(q + c, n, v[i], p.out);
+            }
+        }
+    }
+}
+
+// Gradients at the stored h:  with g = dy w, xhat = h rstd,
+//     dx = rstd (g - xhat mean(g xhat)) + dres,    dw = sum over rows of dy xhat.
+// Both row sums (h^2 and g h) come from one exchange.  A block walks over rows, one row per
+// tpr threads at a time; a thread keeps its columns' share of dw in registers and leaves it
+// in p.part, and a second kernel adds the shares in a fixed order.
+template <typename T, int VEC, int NV, bool AL, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormArgs p, int tpr) {
+    __shared__ float red[64];
+    const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
+    float dw[NV][VEC] = {}, w[NV][VEC];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) w[i][j] = j < n ? p.w[c + j] : 0.f;
+    }
+    const int64_t lane_row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+    const int64_t step = (int64_t)gridDim.x * rpb;
+    // every thread makes the same number of rounds: the sums have block-wide barriers
+    const int64_t rounds = (p.rows + step - 1) / step;
+    for (int64_t k = 0; k < rounds; ++k) {
+        const int64_t row = lane_row + k * step;
+        const bool live = row < p.rows;
+        const int64_t at = row * p.cols;
+        float h[NV][VEC], g[NV][VEC], r[NV][VEC];
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) h[i][j] = g[i][j] = r[i][j] = 0.f;
+            if (live && n > 0) {
+                load_vec<T, VEC, AL>(static_cast<const T *>(p.h) + at + c, n, h[i]);
+                load_vec<T, VEC, AL>(static_cast<const T *>(p.dy) + at + c, n, g[i]);
+                if (p.dres) load_vec<T, VEC, AL>(static_cast<const T *>(p.dres) + at + c, n, r[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                s[0] = fmaf(h[i][j], h[i][j], s[0]);
+                s[1] = fmaf(g[i][j] * w[i][j], h[i][j], s[1]);
+            }
+        row_sum<2>(s, tpr, red);
+        const float rstd = 1.f / sqrtf(s[0] / (float)p.cols + p.eps);
+        const float m = s[1] / (float)p.cols * rstd;  // mean(g xhat)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            float o[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const float xh = h[i][j] * rstd;
+                dw[i][j] = fmaf(g[i][j], xh, dw[i][j]);
+                o[j] = rstd * (g[i][j] * w[i][j] - xh * m) + r[i][j];
+            }
+            if (live && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.dx) + at + c, n, o);
+        }
+    }
+    float *part = p.part + lane_row * p.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (tid + i * tpr) * VEC;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c + j < p.cols) part[c + j] = dw[i][j];
+    }
+}
+
+__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float *part, int64_t parts, int cols,
+                                                           float *dw) {
+    __shared__ float red[8][33];
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (c < cols)
+        for (int64_t r = grp; r < parts; r += 8) s += part[r * cols + c];
+    red[grp][lane] = s;
+    __syncthreads();
+    if (grp == 0 && c < cols) {
+        for (int g = 1; g < 8; ++g) s += red[g][lane];
+        dw[c] = s;
+    }
+}
+
+// Threads per row, vectors per thread and rows per block of a row of `vecs` vectors: the
+// fewest vectors per thread (1, 2 or 4) that keep a row within 256 threads, and four with
+// up to 1024 threads for the longest rows (16384 columns); short rows share a block of 128
+// threads.
+struct RowPlan {
+    int tpr, nv, rpb;
+};
+RowPlan row_plan(int vecs) {
+    RowPlan r{};
+    for (int nv : {1, 2, 4}) {
+        const int t = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+        if (t <= 256 || (nv == 4 && t <= 1024)) {
+            r.tpr = t;
+            r.nv = nv;
+            r.rpb = t < 128 ? 128 / t : 1;
+            return r;
+        }
+    }
+    return r;
+}
+
+bool norm_aligned(const NormArgs &a, size_t e, const void *const *ptrs, int count) {
+    const size_t bytes = 16;
+    for (int i = 0; i < count; ++i)
+        if (!aligned_to(ptrs[i], bytes)) return false;
+    return ((size_t)a.cols * e) % bytes == 0 && aligned_to(a.w, 16);
+}
+
+// f(vectors per thread, most threads per block)
+template <typename F>
+void by_plan(const RowPlan &r, F &&f) {
+    if (r.tpr > 256)
+        f(std::integral_constant<int, 4>(), std::integral_constant<int, 1024>());
+    else if (r.nv == 1)
+        f(std::integral_constant<int, 1>(), std::integral_constant<int, 256>());
+    else if (r.nv == 2)
+        f(std::integral_constant<int, 2>(), std::integral_constant<int, 256>());
+    else
+        f(std::integral_constant<int, 4>(), std::integral_constant<int, 256>());
+}
+
+// Blocks of the backward: enough for every SM to hold its fill of threads, at most one
+// per row; each leaves one row of partial sums per row it works on at a time.
+int64_t bwd_blocks(int64_t rows, const RowPlan &r) {
+    const int64_t want = 152 * (int64_t)(1024 / (r.tpr * r.rpb) > 0 ? 1024 / (r.tpr * r.rpb) : 1);
+    const int64_t most = (rows + r.rpb - 1) / r.rpb;
+    return want < most ? want : most;
+}
+
+}  // namespace
+
+int64_t norm_bwd_parts(int64_t rows, int cols) {
+    const RowPlan r = row_plan((cols + 3) / 4);
+    return r.tpr == 0 ? 0 : bwd_blocks(rows, r) * r.rpb;
+}
+
+cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
+    if (a.rows == 0) return cudaSuccess;
+    const void *ptrs[] = {a.x, a.res, a.h, a.y};
+    const bool bf = dt == KDA_DTYPE_BF16, q = a.out != KDA_NORM_SAME;
+    const bool al = norm_aligned(a, bf ? 2 : 4, ptrs, 4);
+    const int vec = bf ? 8 : 4;
+    const RowPlan r = row_plan((a.cols + vec - 1) / vec);
+    const int64_t blocks = (a.rows + r.rpb - 1) / r.rpb;
+    if (r.tpr == 0 || blocks > INT32_MAX) return cudaErrorInvalidValue;
+    prof_begin("norm_fwd", st);
+    by_plan(r, [&](auto NV, auto MAXT) {
+        const unsigned g = (unsigned)blocks, t = (unsigned)(r.tpr * r.rpb);
+#define KDA_NORM_FWD(T, VEC, AL, Q) norm_fwd_kernel<T, VEC, NV(), AL, Q, MAXT()><<<g, t, 0, st>>>(a, r.tpr)
+        if (bf) {
+            if (al) {
+                if (q) KDA_NORM_FWD(__nv_bfloat16, 8, true, true);
+                else KDA_NORM_FWD(__nv_bfloat16, 8, true, false);
+            } else {
+                if (q) KDA_NORM_FWD(__nv_bfloat16, 8, false, true);
+                else KDA_NORM_FWD(__nv_bfloat16, 8, false, false);
+            }
+        } else if (al) {
+            if (q) KDA_NORM_FWD(float, 4, true, true);
+            else KDA_NORM_FWD(float, 4, true, false);
+        } else {
+            if (q) KDA_NORM_FWD(float, 4, false, true);
+            else KDA_NORM_FWD(float, 4, false, false);
+        }
+#undef KDA_NORM_FWD
+    });
+    prof_end(st);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
+    const bool bf = dt == KDA_DTYPE_BF16;
+    const void *ptrs[] = {a.h, a.dy, a.dres, a.dx};
+    // four columns per thread in both types: dw and the three inputs of eight would not
+    // leave room in registers for a second block
+    bool al = aligned_to(a.w, 4) && ((size_t)a.cols * (bf ? 2 : 4)) % (bf ? 8 : 16) == 0;
+    for (const void *q : ptrs) al = al && aligned_to(q, bf ? 8 : 16);
+    const RowPlan r = row_plan((a.cols + 3) / 4);
+    if (r.tpr == 0) return cudaErrorInvalidValue;
+    const int64_t blocks = bwd_blocks(a.rows, r);
+    if (blocks > 0) {
+        prof_begin("norm_bwd", st);
+        by_plan(r, [&](auto NV, auto MAXT) {
+            const unsigned g = (unsigned)blocks, t = (unsigned)(r.tpr * r.rpb);
+            if (bf) {
+                if (al) norm_bwd_kernel<__nv_bfloat16, 4, NV(), true, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
+                else norm_bwd_kernel<__nv_bfloat16, 4, NV(), false, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
+            } else {
+                if (al) norm_bwd_kernel<float, 4, NV(), true, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
+                else norm_bwd_kernel<float, 4, NV(), false, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
+            }
+        });
+        prof_end(st);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    prof_begin("norm_bwd_sum", st);
+    norm_bwd_sum_kernel<<<(unsigned)((a.cols + 31) / 32), 256, 0, st>>>(a.part, blocks * r.rpb, a.cols,
+                                                                        a.dw);
+    prof_end(st);
+    return cudaGetLastError();
+}
+
+}  // namespace kda

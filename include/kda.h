@@ -27,6 +27,11 @@
  *                      that keeps the backward's recomputed state) without the
  *                      recompute
  *
+ * Beside KDA itself, the rest of a recurrent block (see "The recurrent block"):
+ *   kda_short_conv_fwd / _bwd / _step   the short causal convolution
+ *   kda_ssm_scan_fwd / _bwd, kda_ssm_step   the selective state-space scan
+ *   kda_add_rmsnorm_fwd / _bwd          residual addition and RMS norm, 8-bit outputs
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Memory.  Every tensor pointer is a DEVICE pointer owned by the caller, on
@@ -158,6 +163,9 @@ typedef enum {
                                                finite; that chunk's gradients were not
                                                computed.  Reported as
                                                KDA_ERR_UNSUPPORTED                     */
+#define KDA_DEVICE_BAD_INDEX      (1 << 4)  /* a state index past the last slot (the step
+                                               entry points); that row was skipped.
+                                               Reported as KDA_ERR_INVALID_ARG         */
 
 typedef struct {
     int32_t B, T, H, HV, K, V;  /* see Layouts; HV % H == 0                         */
@@ -439,6 +447,171 @@ kda_status kda_chunk_fwd_save(const void *q, const void *k, const void *v, const
  * kda_chunk_workspace_size, a shape that may be packed (B == 1) is sized for packed
  * input, which covers a dense call of the same shape too. */
 size_t kda_chunk_bwd_workspace_size(const kda_shape *shape);
+
+/* ------------------------------------------------------------------------------
+ * The recurrent block around KDA: the short causal convolution in front of the state
+ * update, the selective state-space scan (the delta rule's sibling: one decay per head
+ * and no delta correction), and the residual RMS norm at the block's entry.
+ *
+ * Conventions are those above (device pointers, streams, errors, packed sequences),
+ * with these additions.
+ * Strides.  Inputs that a layer cuts out of one projection may be column ranges of a
+ * wider tensor: x_stride etc. are the elements between the rows of consecutive tokens
+ * (0: contiguous rows); the columns of a row are contiguous and row (b, t) is row
+ * b * T + t.  Outputs are contiguous.  Any alignment of the element type is taken;
+ * rows that start on 16-byte boundaries are faster.
+ * State caches.  The step entry points update one row of a cache per batch row, in
+ * place: state_indices[n] is row n's slot (NULL: slot n).  A negative entry marks an
+ * unused batch row: no state is touched and its output is zero.  An entry past the last
+ * slot sets KDA_DEVICE_BAD_INDEX, and its row is skipped like an unused one.  Entries must be distinct: two
+ * rows of one slot race.
+ * Non-finite inputs make the values that depend on them non-finite and no others.
+ */
+
+/* flags of kda_conv_shape */
+#define KDA_CONV_FLAG_SILU (1u << 0)      /* y = pre * sigmoid(pre); without it y = pre */
+
+typedef struct {
+    int32_t B, T, C, W;         /* W taps: 2, 3 or 4                                    */
+    int32_t num_seqs;           /* N: B when dense, len(cu_seqlens) - 1 when packed      */
+    kda_dtype dtype;            /* of x, y, the states and their gradients              */
+    int64_t x_stride;           /* elements between x's rows (0: C)                     */
+    uint32_t flags;             /* KDA_CONV_FLAG_*                                      */
+} kda_conv_shape;
+
+/*
+ * kda_short_conv_fwd -- y_t[c] = act(bias[c] + sum_{k < W} w[c, k] x_{t-W+1+k}[c]), rows
+ * before a sequence's first being its carried state (or zero).
+ *   x          [B, T, C];  w [C, W] fp32;  bias [C] fp32 or NULL
+ *   state_in   [N, W-1, C] or NULL (zeros): the rows before each sequence, oldest first
+ *   y          [B, T, C]; rows outside every sequence are not written
+ *   state_out  [N, W-1, C] or NULL: the last W-1 rows of (state_in, x) per sequence (an
+ *              empty sequence keeps its state).  Must not alias state_in.
+ */
+kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias,
+                              const void *state_in, const int32_t *cu_seqlens,
+                              const kda_conv_shape *shape, void *y, void *state_out,
+                              int32_t *dev_status, kda_stream_t stream);
+/*
+ * kda_short_conv_bwd -- the gradients for dy = dL/dy and dstate_out = dL/dstate_out (or
+ * NULL): dx [B, T, C] and dstate_in [N, W-1, C] (or NULL, not stored) in the shape's type, dw [C, W] and
+ * dbias [C] (or NULL) fp32, summed in a fixed order.  With cu_seqlens, dx is zero in rows
+ * outside every sequence.
+ *   workspace  kda_short_conv_bwd_workspace_size() bytes, 16-byte aligned.
+ */
+kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias,
+                              const void *state_in, const int32_t *cu_seqlens,
+                              const kda_conv_shape *shape, const void *dy, const void *dstate_out,
+                              void *dx, float *dw, float *dbias, void *dstate_in, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_status, kda_stream_t stream);
+size_t kda_short_conv_bwd_workspace_size(const kda_conv_shape *shape);
+/*
+ * kda_short_conv_step -- one token for each of shape->B batch rows (T = 1): y [B, C] and
+ * the state cache [num_slots, W-1, C] moved on by one row, in place.
+ */
+kda_status kda_short_conv_step(const void *x, const float *w, const float *bias, void *state,
+                               const int32_t *state_indices, int32_t num_slots,
+                               const kda_conv_shape *shape, void *y, int32_t *dev_status,
+                               kda_stream_t stream);
+
+/* flags of kda_ssm_shape */
+#define KDA_SSM_FLAG_DT_SOFTPLUS (1u << 0) /* the step is softplus(dt + dt_bias), not
+                                              dt + dt_bias                              */
+
+typedef struct {
+    int32_t B, T, H, G, N, P;   /* H heads in G groups (H % G == 0), N state rows and P
+                                   columns per head: 1 <= N, P <= 256                   */
+    int32_t num_seqs;           /* B when dense, len(cu_seqlens) - 1 when packed        */
+    kda_dtype dtype;            /* of x, dt, Bm, Cm, y and their gradients              */
+    int64_t x_stride, dt_stride, b_stride, c_stride;  /* elements between rows (0:
+                                   contiguous: H P, H, G N, G N)                        */
+    uint32_t flags;             /* KDA_SSM_FLAG_*                                       */
+} kda_ssm_shape;
+
+/*
+ * kda_ssm_scan_fwd -- the selective state-space scan.  Per sequence and head h, with B_t,
+ * C_t from group h / (H / G), step d_t (see the flag) and A = -exp(A_log[h]):
+ *     S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T,      y_t = S_t^T C_t + D[h] x_t
+ *   x          [B, T, H, P];  dt [B, T, H];  Bm, Cm [B, T, G, N]
+ *   A_log      [H] fp32;  D, dt_bias [H] fp32 or NULL
+ *   h0, ht     [num_seqs, H, N, P] fp32 or NULL, as for kda_chunk_fwd; ht may alias h0
+ *   y          [B, T, H, P]; rows outside every sequence are not written
+ *   workspace  kda_ssm_workspace_size() bytes, 256-byte aligned.  It holds the state at
+ *              each chunk's start on return: kda_ssm_scan_bwd takes it as `saved`.
+ * Steps that are >= 0 keep every decay <= 1; they are not checked.
+ */
+kda_status kda_ssm_scan_fwd(const void *x, const void *dt, const float *A_log, const void *Bm,
+                            const void *Cm, const float *D, const float *dt_bias, const float *h0,
+                            const int32_t *cu_seqlens, const kda_ssm_shape *shape, void *y,
+                            float *ht, void *workspace, size_t workspace_bytes,
+                            int32_t *dev_status, kda_stream_t stream);
+size_t kda_ssm_workspace_size(const kda_ssm_shape *shape);
+/*
+ * kda_ssm_scan_bwd -- the gradients for dy = dL/dy and dht = dL/dht (or NULL): dx, ddt,
+ * dB, dC in the shape's type and the inputs' (contiguous) layouts; dA_log, dD, ddt_bias
+ * [H] fp32 (dD, ddt_bias may be NULL: not stored); dh0 [num_seqs, H, N, P] fp32 or NULL.
+ * dB and dC are summed over a group's heads, the [H] gradients over all tokens, each in a
+ * fixed order.  With cu_seqlens, rows outside every sequence are zero.
+ *   saved      the workspace of kda_ssm_scan_fwd for the same inputs and shape, untouched
+ *              since, or NULL: the chunk states are formed again
+ *   workspace  kda_ssm_bwd_workspace_size(shape, saved != NULL) bytes, 256-byte aligned.
+ */
+kda_status kda_ssm_scan_bwd(const void *x, const void *dt, const float *A_log, const void *Bm,
+                            const void *Cm, const float *D, const float *dt_bias, const float *h0,
+                            const int32_t *cu_seqlens, const kda_ssm_shape *shape, const void *dy,
+                            const float *dht, void *dx, void *ddt, void *dB, void *dC,
+                            float *dA_log, float *dD, float *ddt_bias, float *dh0,
+                            const void *saved, void *workspace, size_t workspace_bytes,
+                            int32_t *dev_status, kda_stream_t stream);
+size_t kda_ssm_bwd_workspace_size(const kda_ssm_shape *shape, int saved);
+/*
+ * kda_ssm_step -- one token for each of shape->B batch rows (T = 1): y [B, H, P] and the
+ * state cache [num_slots, H, N, P] fp32 advanced in place.
+ */
+kda_status kda_ssm_step(const void *x, const void *dt, const float *A_log, const void *Bm,
+                        const void *Cm, const float *D, const float *dt_bias, float *state,
+                        const int32_t *state_indices, int32_t num_slots,
+                        const kda_ssm_shape *shape, void *y, int32_t *dev_status,
+                        kda_stream_t stream);
+
+typedef enum {
+    KDA_NORM_SAME = 0,          /* y in the input's type                                */
+    KDA_NORM_E4M3 = 1,          /* 8-bit floats (4 exponent bits, 3 fraction bits), top 448 */
+    KDA_NORM_INT8 = 2           /* 8-bit integers, top 127                              */
+} kda_norm_out;
+
+typedef struct {
+    int64_t rows;
+    int32_t cols;               /* 1 .. 16384                                           */
+    kda_dtype dtype;            /* of x, residual, h and their gradients                */
+    kda_norm_out out;
+    int32_t group;              /* 8-bit outputs: columns per scale: 0 (the row) or 128 */
+    float eps;                  /* >= 0                                                 */
+} kda_norm_shape;
+
+/*
+ * kda_add_rmsnorm_fwd -- h = x + residual (residual NULL: h = x),
+ *     y = h w / sqrt(mean(h^2) + eps),
+ * and for the 8-bit outputs, per row or group of columns, scale = max|y| / top (1 where
+ * that is 0 or not a number) and y rounded to q = y / scale, ties to even.
+ *   x, residual, h  [rows, cols] (h may be NULL: not stored); the norm takes the unrounded sum
+ *   w               [cols] fp32
+ *   y               [rows, cols]: the shape's type, or one byte per element
+ *   scale           [rows, groups] fp32, groups = ceil(cols / group) (1 without); 8-bit only
+ */
+kda_status kda_add_rmsnorm_fwd(const void *x, const void *residual, const float *w,
+                               const kda_norm_shape *shape, void *h, void *y, float *scale,
+                               kda_stream_t stream);
+/*
+ * kda_add_rmsnorm_bwd -- the gradients at the stored h for dy = dL/dy and dh = dL/dh of
+ * the residual stream (or NULL): dx [rows, cols] (x's and the residual's alike) in the
+ * shape's type, dw [cols] fp32 summed in a fixed order.  shape->out and group are ignored.
+ *   workspace  kda_add_rmsnorm_bwd_workspace_size() bytes, 16-byte aligned.
+ */
+kda_status kda_add_rmsnorm_bwd(const void *dy, const void *h, const float *w, const void *dh,
+                               const kda_norm_shape *shape, void *dx, float *dw, void *workspace,
+                               size_t workspace_bytes, kda_stream_t stream);
+size_t kda_add_rmsnorm_bwd_workspace_size(const kda_norm_shape *shape);
 
 /*
  * kda_read_device_status -- synchronise `stream`, copy the status word to
