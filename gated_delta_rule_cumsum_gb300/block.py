@@ -224,17 +224,18 @@ def _on_device(fn):
     `stream`, if given, as the current stream: outputs, workspaces and contiguous copies
     then belong to the stream whose kernels use them."""
     @functools.wraps(fn)
-    def wrapper(first, *args, **kwargs):
-        if not first.is_cuda:
+    def wrapper(*args, **kwargs):
+        first = args[0] if args else next((t for t in kwargs.values() if isinstance(t, torch.Tensor)), None)
+        if first is None or not first.is_cuda:
             _bad("tensors must be on a CUDA device")
         stream = kwargs.get("stream")
         if stream is not None:
             with torch.cuda.stream(stream):
-                return fn(first, *args, **kwargs)
+                return fn(*args, **kwargs)
         if first.device.index == torch.cuda.current_device():
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
         with torch.cuda.device(first.device):
-            return fn(first, *args, **kwargs)
+            return fn(*args, **kwargs)
     return wrapper
 
 

@@ -57,12 +57,16 @@ __device__ __forceinline__ float step_size(float raw, float bias, int softplus) 
     return softplus ? softplus_f(v) : v;
 }
 
-// d_i, a_i (log2, cumulative) of a chunk's rows in shared memory; rows past nr have d = 0
-// and the last row's a.  All threads call; ends with a barrier.
+// d_i and a_i (log2, cumulative) of a chunk's rows in shared memory; rows past nr have d = 0
+// and the last row's a.  a is kept as a sum of two floats, a + lo: under strong decay a_i runs
+// to thousands while the rows next to each other still differ by little, and the difference
+// of two single floats would lose those digits.  All threads call; ends with a barrier.
 template <typename T>
 __device__ __forceinline__ void chunk_decays(const SsmArgs &p, const Chunk &c, int h, float *d,
-                                             float *a) {
+                                             float *a, float *lo) {
+    __shared__ double first_half;
     const int i = threadIdx.x;
+    double s = 0.0;
     if (i < kL) {
         float v = 0.f;
         if (i < c.nr) {
@@ -70,17 +74,25 @@ __device__ __forceinline__ void chunk_decays(const SsmArgs &p, const Chunk &c, i
             v = step_size(raw, p.dt_bias ? p.dt_bias[h] : 0.f, p.softplus);
         }
         d[i] = v;
-        float s = v * (-expf(p.A_log[h]) * kLog2e);
+        s = v * (-expf(p.A_log[h]) * kLog2e);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, s, o);
+            const double u = __shfl_up_sync(0xffffffffu, s, o);
             if ((i & 31) >= o) s += u;
         }
-        a[i] = s;
+        if (i == 31) first_half = s;
     }
     __syncthreads();
-    if (i >= 32 && i < kL) a[i] += a[31];
+    if (i < kL) {
+        if (i >= 32) s += first_half;
+        a[i] = (float)s;
+        lo[i] = (float)(s - (double)a[i]);
+    }
     __syncthreads();
+}
+// 2^{a_i - a_j}
+__device__ __forceinline__ float decay_between(const float *a, const float *lo, int i, int j) {
+    return ex2_ftz((a[i] - a[j]) + (lo[i] - lo[j]));
 }
 
 // A 64 x 64 tile of a row-major matrix into shared memory, zero outside rows x cols, each
@@ -118,7 +130,7 @@ __device__ __forceinline__ void mm64(float (&acc)[4][4], const float *A, const f
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(256) ssm_chunk_state_kernel(SsmArgs p) {
     extern __shared__ float sm[];
-    float *As = sm, *Bs = sm + kTile, *d = Bs + kTile, *a = d + kL, *wgt = a + kL;
+    float *As = sm, *Bs = sm + kTile, *d = Bs + kTile, *a = d + kL, *lo = a + kL, *wgt = lo + kL;
     const int nt = (p.Ns + kL - 1) / kL, pt = (p.P + kL - 1) / kL;
     int64_t id = blockIdx.x;
     const int p0 = (int)(id % pt) * kL;
@@ -130,10 +142,10 @@ __global__ void __launch_bounds__(256) ssm_chunk_state_kernel(SsmArgs p) {
     Chunk c;
     if (!find_chunk(p, slot, c)) return;
     const int g = h / (p.H / p.G);
-    chunk_decays<T>(p, c, h, d, a);
+    chunk_decays<T>(p, c, h, d, a, lo);
     if (threadIdx.x < kL) {
         const int i = threadIdx.x;
-        wgt[i] = BWD ? ex2_ftz(a[i]) : ex2_ftz(a[kL - 1] - a[i]) * d[i];
+        wgt[i] = BWD ? ex2_ftz(a[i]) : decay_between(a, lo, kL - 1, i) * d[i];
     }
     __syncthreads();
     const int ncols = min(kL, p.Ns - n0), pcols = min(kL, p.P - p0);
@@ -244,6 +256,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) ssm_chunk_out_kernel(SsmArgs p) {
     extern __shared__ float sm[];
     float *Ct = sm, *Bt = Ct + kTile, *Sx = Bt + kTile, *d = Sx + kTile, *a = d + kL;
+    float *lo = a + kL;
     const int pt = (p.P + kL - 1) / kL;
     int64_t id = blockIdx.x;
     const int p0 = (int)(id % pt) * kL;
@@ -254,7 +267,7 @@ __global__ void __launch_bounds__(256) ssm_chunk_out_kernel(SsmArgs p) {
     if (!find_chunk(p, slot, c)) return;
     const int g = h / (p.H / p.G), pcols = min(kL, p.P - p0);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    chunk_decays<T>(p, c, h, d, a);
+    chunk_decays<T>(p, c, h, d, a, lo);
     const int64_t unit = slot * p.H + h;
     float gram[4][4] = {}, y[4][4] = {};
     for (int n0 = 0; n0 < p.Ns; n0 += kL) {
@@ -277,7 +290,7 @@ __global__ void __launch_bounds__(256) ssm_chunk_out_kernel(SsmArgs p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int s = 4 * tx + j;
-            Ct[s * kLD + r] = s <= r ? gram[i][j] * ex2_ftz(a[r] - a[s]) * d[s] : 0.f;
+            Ct[s * kLD + r] = s <= r ? gram[i][j] * decay_between(a, lo, r, s) * d[s] : 0.f;
             y[i][j] *= er;
         }
     }
@@ -303,18 +316,19 @@ __global__ void __launch_bounds__(256) ssm_chunk_out_kernel(SsmArgs p) {
 //     dx_j = sum_i G_ij e_ij d_j dy_i + d_j 2^{a_end - a_j} E^T B_j + D dy_j
 //     dC_i = sum_j Z_ij e_ij d_j B_j + 2^{a_i} S dy_i
 //     dB_j = sum_i Z_ij e_ij d_j C_i + d_j 2^{a_end - a_j} E x_j
-// and, through the exponents a (natural units), with Q_ij = Z_ij G_ij e_ij d_j,
+// and, through the exponents, with Q_ij = Z_ij G_ij e_ij d_j,
 // u_i = 2^{a_i} C_i . S dy_i and v_j = d_j 2^{a_end - a_j} B_j . E x_j:
-//     da_i = sum_j Q_ij - sum_k Q_ki + u_i - v_i,  and at the last row also
-//            sum_j v_j + 2^{a_end} <E, S>;
-//     the decay of row t gets l_t = sum_{i >= t} da_i, and
+// the log decay of row t (which every pair i >= t > j passes) gets
+//     l_t = sum_{i >= t > j} Q_ij + sum_{i >= t} u_i + sum_{j < t} v_j + 2^{a_end} <E, S>,
 //     dd_t = A l_t + sum_i Q_it / d_t + v_t / d_t,   dA = sum_t d_t l_t.
+// l_t is summed term by term: taken as a running difference of row and column sums, a pair
+// far from t would leave its rounding in l_t, which a strong decay's A d_t then multiplies.
 // (The quotients are formed without the division.)
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_chunk_grads_kernel(SsmArgs p) {
     extern __shared__ float sm[];
     float *M = sm, *W = M + kTile, *X = W + kTile, *Y = X + kTile, *d = Y + kTile, *a = d + kL;
-    float *ea = a + kL, *el = ea + kL, *da = el + kL, *dd = da + kL, *red = dd + kL;  // red: 16 x 64
+    float *lo = a + kL, *ea = lo + kL, *el = ea + kL, *l = el + kL, *dd = l + kL, *red = dd + kL;  // red: 16 x 64
     const int h = (int)(blockIdx.x % p.H);
     const int64_t slot = blockIdx.x / p.H;
     Chunk c;
@@ -326,10 +340,10 @@ __global__ void __launch_bounds__(256) ssm_chunk_grads_kernel(SsmArgs p) {
     const T *xg = static_cast<const T *>(p.x) + c.r0 * p.x_stride + (int64_t)h * p.P;
     const T *dyg = static_cast<const T *>(p.dy) + (c.r0 * p.H + h) * p.P;
     const int64_t ys = (int64_t)p.H * p.P;
-    chunk_decays<T>(p, c, h, d, a);
+    chunk_decays<T>(p, c, h, d, a, lo);
     if (tid < kL) {
         ea[tid] = ex2_ftz(a[tid]);
-        el[tid] = ex2_ftz(a[kL - 1] - a[tid]);
+        el[tid] = decay_between(a, lo, kL - 1, tid);
     }
     float G[4][4] = {}, Z[4][4] = {};
     for (int n0 = 0; n0 < p.Ns; n0 += kL) {
@@ -347,36 +361,58 @@ __global__ void __launch_bounds__(256) ssm_chunk_grads_kernel(SsmArgs p) {
         mm64(Z, X, Y);
         __syncthreads();
     }
-    // M_ij = G_ij e_ij d_j, W_ij = Z_ij e_ij d_j; row and column sums of Q
+    // M_ij = G_ij e_ij d_j, W_ij = Z_ij e_ij d_j; Q below the diagonal, and its column sums
     float col[4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
-        float row = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int s = 4 * tx + j;
-            const float e = s <= r ? ex2_ftz(a[r] - a[s]) : 0.f;
+            const float e = s <= r ? decay_between(a, lo, r, s) : 0.f;
             if (s == r) dD += Z[i][j];
             M[r * kLD + s] = G[i][j] * e * d[s];
             W[r * kLD + s] = Z[i][j] * e * d[s];
             const float q = Z[i][j] * G[i][j] * e;
-            row = fmaf(q, d[s], row);
+            X[r * kLD + s] = s < r ? q * d[s] : 0.f;
             col[j] += q;
         }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) row += __shfl_xor_sync(0xffffffffu, row, o);
-        if (tx == 0) da[r] = row;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) red[ty * kL + 4 * tx + j] = col[j];
     __syncthreads();
+    {   // each row's sums over the columns before t, four threads a row
+        float *q = X + (tid >> 2) * kLD + 16 * (tid & 3), s[16], run = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            s[k] = run;
+            run += q[k];
+        }
+        float before = run;
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, before, o, 4);
+            if ((tid & 3) >= o) before += x;
+        }
+        before = __shfl_up_sync(0xffffffffu, before, 1, 4);
+        if ((tid & 3) == 0) before = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) q[k] = before + s[k];
+    }
     if (tid < kL) {
         float s = 0.f;
         for (int k = 0; k < 16; ++k) s += red[k * kL + tid];
         dd[tid] = s;            // sum_i Q_it / d_t
-        da[tid] -= s * d[tid];
     }
+    __syncthreads();
+    {   // sum_{i >= t} sum_{j < t} Q_ij, sixteen rows a thread
+        const int c0 = tid & (kL - 1), r0 = 16 * (tid >> 6);
+        float s = 0.f;
+        for (int r = max(r0, c0); r < r0 + 16; ++r) s += X[r * kLD + c0];
+        red[tid] = s;
+    }
+    __syncthreads();
+    if (tid < kL) l[tid] = (red[tid] + red[kL + tid]) + (red[2 * kL + tid] + red[3 * kL + tid]);
     const float D = p.D ? p.D[h] : 0.f;
     // dx, 64 columns at a time
     for (int p0 = 0; p0 < p.P; p0 += kL) {
@@ -490,8 +526,8 @@ __global__ void __launch_bounds__(256) ssm_chunk_grads_kernel(SsmArgs p) {
     for (int i = 0; i < 4; ++i)
         if (tx == 0) {
             const int r = 4 * ty + i;
-            da[r] += u[i] - v[i] * d[r];
             dd[r] += v[i];
+            ea[r] = u[i];          // read above for the last time, but for the last row's
             red[r] = v[i] * d[r];
         }
     // block sums: <E, S> and dD
@@ -505,32 +541,41 @@ __global__ void __launch_bounds__(256) ssm_chunk_grads_kernel(SsmArgs p) {
         red[kL + 8 + (tid >> 5)] = dD;
     }
     __syncthreads();
-    if (tid < 32) {  // rows tid and tid + 32: the sums from the right
-        float vs = red[tid] + red[tid + 32], e = tid < 8 ? red[kL + tid] : 0.f;
-        float dds = tid < 8 ? red[kL + 8 + tid] : 0.f;
+    if (tid < 32) {  // rows tid and tid + 32
+        float e = tid < 8 ? red[kL + tid] : 0.f, dds = tid < 8 ? red[kL + 8 + tid] : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            vs += __shfl_xor_sync(0xffffffffu, vs, o);
             e += __shfl_xor_sync(0xffffffffu, e, o);
             dds += __shfl_xor_sync(0xffffffffu, dds, o);
         }
-        float hi = da[tid + 32], lo = da[tid];
+        // u from the right (with the row itself), v from the left (without it)
+        float u0 = ea[tid], u1 = ea[tid + 32], v0 = red[tid], v1 = red[tid + 32];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const float x = __shfl_down_sync(0xffffffffu, hi, o), y = __shfl_down_sync(0xffffffffu, lo, o);
+            const float x0 = __shfl_down_sync(0xffffffffu, u0, o), x1 = __shfl_down_sync(0xffffffffu, u1, o);
+            const float y0 = __shfl_up_sync(0xffffffffu, v0, o), y1 = __shfl_up_sync(0xffffffffu, v1, o);
             if (tid + o < 32) {
-                hi += x;
-                lo += y;
+                u0 += x0;
+                u1 += x1;
+            }
+            if (tid >= o) {
+                v0 += y0;
+                v1 += y1;
             }
         }
-        lo += __shfl_sync(0xffffffffu, hi, 0);
-        const float end = vs + ea[kL - 1] * e;
+        u0 += __shfl_sync(0xffffffffu, u1, 0);
+        const float half = __shfl_sync(0xffffffffu, v0, 31);
+        v0 = __shfl_up_sync(0xffffffffu, v0, 1);
+        v1 = __shfl_up_sync(0xffffffffu, v1, 1);
+        if (tid == 0) v0 = v1 = 0.f;
+        const float end = ex2_ftz(a[kL - 1]) * e;
+        const float l0 = l[tid] + (u0 + (v0 + end)), l1 = l[tid + 32] + (u1 + (half + v1 + end));
         const float A = -expf(p.A_log[h]), bias = p.dt_bias ? p.dt_bias[h] : 0.f;
         float sA = 0.f, sb = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int t = tid + 32 * k;
-            const float l = (k ? hi : lo) + end;
+            const float l = k ? l1 : l0;
             if (t < c.nr) {
                 const int64_t row = c.r0 + t;
                 float gd = fmaf(A, l, dd[t]);
@@ -664,9 +709,9 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmStepArgs p) {
     }
 }
 
-constexpr size_t kSmemState = (2 * kTile + 3 * kL) * 4;
-constexpr size_t kSmemOut = (3 * kTile + 2 * kL) * 4;
-constexpr size_t kSmemGrads = (4 * kTile + 6 * kL + 16 * kL) * 4;
+constexpr size_t kSmemState = (2 * kTile + 4 * kL) * 4;
+constexpr size_t kSmemOut = (3 * kTile + 3 * kL) * 4;
+constexpr size_t kSmemGrads = (4 * kTile + 7 * kL + 16 * kL) * 4;
 
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {

@@ -1,0 +1,140 @@
+"""Host-side refusals of the recurrent block's operators: nothing is enqueued, no GPU is
+needed."""
+import ctypes
+
+import pytest
+import torch
+
+FAKE = 0x1000  # never dereferenced: the host checks fail first
+
+
+@pytest.fixture(scope="module")
+def kda():
+    from gated_delta_rule_cumsum_gb300 import build as b
+
+    b.build()
+    import gated_delta_rule_cumsum_gb300 as kda
+
+    kda.load()
+    return kda
+
+
+def conv(kda, **kw):
+    return kda.KdaConvShape(**{**dict(B=1, T=8, C=16, W=4, num_seqs=1, dtype=1, x_stride=0, flags=1), **kw})
+
+
+def ssm(kda, **kw):
+    return kda.KdaSsmShape(**{**dict(B=1, T=8, H=4, G=2, N=16, P=8, num_seqs=1, dtype=1, x_stride=0,
+                                     dt_stride=0, b_stride=0, c_stride=0, flags=1), **kw})
+
+
+def norm(kda, **kw):
+    return kda.KdaNormShape(**{**dict(rows=4, cols=16, dtype=1, out=0, group=0, eps=1e-6), **kw})
+
+
+def said(kda, status, want):
+    assert status == want, kda.kda_last_error_message()
+    assert kda.kda_last_error_message()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 1), (dict(T=-1), 1), (dict(C=0), 1), (dict(W=1), 2), (dict(W=5), 2), (dict(num_seqs=2), 1),
+    (dict(dtype=9), 1), (dict(flags=4), 2), (dict(x_stride=15), 1), (dict(B=70000, T=70000, num_seqs=70000), 2)])
+def test_conv_refusals(kda, kw, status):
+    s = ctypes.byref(conv(kda, **kw))
+    lib = kda.load()
+    said(kda, lib.kda_short_conv_fwd(FAKE, FAKE, None, None, None, s, FAKE, None, None, None), status)
+    said(kda, lib.kda_short_conv_bwd(FAKE, FAKE, None, None, None, s, FAKE, None, FAKE, FAKE, None, None,
+                                     FAKE, 1 << 30, None, None), status)
+
+
+def test_conv_pointer_refusals(kda):
+    lib, s = kda.load(), ctypes.byref(conv(kda))
+    said(kda, lib.kda_short_conv_fwd(FAKE, None, None, None, None, s, FAKE, None, None, None), 1)
+    said(kda, lib.kda_short_conv_fwd(FAKE, FAKE, None, FAKE, None, s, FAKE, FAKE, None, None), 1)  # aliased state
+    packed = ctypes.byref(conv(kda, B=2, num_seqs=1))
+    said(kda, lib.kda_short_conv_fwd(FAKE, FAKE, None, None, FAKE, packed, FAKE, None, None, None), 1)
+    need = kda.kda_short_conv_bwd_workspace_size(conv(kda))
+    assert need > 0
+    said(kda, lib.kda_short_conv_bwd(FAKE, FAKE, None, None, None, s, FAKE, None, FAKE, FAKE, None, None,
+                                     FAKE, need - 1, None, None), 1)
+    said(kda, lib.kda_short_conv_bwd(FAKE, FAKE, None, None, None, s, FAKE, None, FAKE, FAKE, None, None,
+                                     FAKE + 4, need, None, None), 1)
+    said(kda, lib.kda_short_conv_step(FAKE, FAKE, None, FAKE, FAKE, 4, s, FAKE, None, None), 1)  # T != 1
+    one = ctypes.byref(conv(kda, B=8, T=1, num_seqs=8))
+    said(kda, lib.kda_short_conv_step(FAKE, FAKE, None, FAKE, None, 7, one, FAKE, None, None), 1)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), 1), (dict(H=3), 1), (dict(G=0), 1), (dict(N=0), 1), (dict(N=257), 2), (dict(P=257), 2),
+    (dict(num_seqs=3), 1), (dict(dtype=2), 1), (dict(flags=2), 2), (dict(x_stride=31), 1), (dict(dt_stride=3), 1),
+    (dict(b_stride=31), 1), (dict(c_stride=-1), 1)])
+def test_ssm_refusals(kda, kw, status):
+    s, lib = ssm(kda, **kw), kda.load()
+    r = ctypes.byref(s)
+    said(kda, lib.kda_ssm_scan_fwd(FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, None, r, FAKE, None, FAKE,
+                                   1 << 40, None, None), status)
+    said(kda, lib.kda_ssm_scan_bwd(FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, None, r, FAKE, None, FAKE,
+                                   FAKE, FAKE, FAKE, FAKE, None, None, None, None, FAKE, 1 << 40, None, None),
+         status)
+    if kw.keys() <= {"B", "H", "G", "N", "P"}:
+        assert kda.kda_ssm_workspace_size(s) == 0 and kda.kda_ssm_bwd_workspace_size(s, False) == 0
+
+
+def test_ssm_workspace_refusals(kda):
+    s, lib = ssm(kda), kda.load()
+    r = ctypes.byref(s)
+    need, back = kda.kda_ssm_workspace_size(s), kda.kda_ssm_bwd_workspace_size(s, True)
+    assert need > 0 and kda.kda_ssm_bwd_workspace_size(s, False) == back + need
+    args = (FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, None, r)
+    said(kda, lib.kda_ssm_scan_fwd(*args, FAKE, None, FAKE, need - 1, None, None), 1)
+    said(kda, lib.kda_ssm_scan_fwd(*args, FAKE, None, FAKE + 16, need, None, None), 1)
+    grads = (FAKE, None, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None)
+    said(kda, lib.kda_ssm_scan_bwd(*args, *grads, FAKE, FAKE, back - 1, None, None), 1)
+    said(kda, lib.kda_ssm_scan_bwd(*args, *grads, FAKE + 16, FAKE, back, None, None), 1)
+    said(kda, lib.kda_ssm_step(FAKE, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, FAKE, 4, r, FAKE, None, None), 1)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), 1), (dict(cols=0), 1), (dict(cols=16385), 2), (dict(dtype=5), 1), (dict(out=3), 1),
+    (dict(group=64), 2), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1)])
+def test_norm_refusals(kda, kw, status):
+    lib, s = kda.load(), ctypes.byref(norm(kda, **kw))
+    said(kda, lib.kda_add_rmsnorm_fwd(FAKE, None, FAKE, s, None, FAKE, FAKE, None), status)
+    if "out" not in kw and "group" not in kw:
+        said(kda, lib.kda_add_rmsnorm_bwd(FAKE, FAKE, FAKE, None, s, FAKE, FAKE, FAKE, 1 << 30, None), status)
+
+
+def test_norm_pointer_refusals(kda):
+    lib = kda.load()
+    s = ctypes.byref(norm(kda, out=1))
+    said(kda, lib.kda_add_rmsnorm_fwd(FAKE, None, FAKE, s, None, FAKE, None, None), 1)  # no scale
+    need = kda.kda_add_rmsnorm_bwd_workspace_size(norm(kda))
+    assert need > 0
+    s = ctypes.byref(norm(kda))
+    said(kda, lib.kda_add_rmsnorm_bwd(FAKE, FAKE, FAKE, None, s, FAKE, FAKE, FAKE, need - 1, None), 1)
+    said(kda, lib.kda_add_rmsnorm_bwd(FAKE, FAKE, FAKE, None, s, FAKE, FAKE, FAKE + 8, need, None), 1)
+
+
+def test_binding_refuses_host_tensors(kda):
+    x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
+    for call in (lambda: kda.short_conv(x, w), lambda: kda.add_rms_norm(x, torch.ones(8)),
+                 lambda: kda.short_conv_step(x[:, 0], torch.zeros(1, 3, 8), w),
+                 lambda: kda.ssm_scan(x[..., None], x, torch.zeros(8), x[..., None], x[..., None])):
+        with pytest.raises(kda.KdaError):
+            call()
+
+
+def test_rows_are_read_in_place_where_they_can_be(kda):
+    rows = kda.block._rows
+    wide = torch.zeros(3, 5, 40)
+    assert rows(wide, 2) == (wide, 0) or rows(wide, 2)[1] == 0
+    part = wide[..., 8:20]
+    assert rows(part, 2)[0] is part and rows(part, 2)[1] == 40
+    heads = part.unflatten(-1, (3, 4))
+    assert rows(heads, 2)[0] is heads and rows(heads, 2)[1] == 40
+    for t in (wide.transpose(0, 1), wide[:, ::2], wide[..., ::2], wide[:1].expand(3, 5, 40)):
+        got, step = rows(t, 2)
+        assert got.is_contiguous() and step == 0 and torch.equal(got, t)
+    some = wide[1:2, ::2]  # one sequence: every second row, evenly spaced
+    assert rows(some, 2)[0] is some and rows(some, 2)[1] == 80
