@@ -81,7 +81,9 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _s(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    # the raw handle: current_stream() builds a Stream object, 3 us of a decode call
+    return (torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None
+            else stream.cuda_stream)
 
 
 def _nbytes(t: Optional[torch.Tensor]) -> int:
@@ -226,17 +228,26 @@ def _on_device(fn):
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
         first = args[0] if args else next((t for t in kwargs.values() if isinstance(t, torch.Tensor)), None)
-        if first is None or not first.is_cuda:
+        dev = -1 if first is None else first.get_device()
+        if dev < 0:
             _bad("tensors must be on a CUDA device")
         stream = kwargs.get("stream")
         if stream is not None:
             with torch.cuda.stream(stream):
                 return fn(*args, **kwargs)
-        if first.device.index == torch.cuda.current_device():
+        if dev == torch.cuda.current_device():
             return fn(*args, **kwargs)
-        with torch.cuda.device(first.device):
+        with torch.cuda.device(dev):
             return fn(*args, **kwargs)
     return wrapper
+
+
+def _same_device(first, *ts):
+    """Every given tensor on first's (CUDA) device, else KdaError."""
+    dev = first.get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            _one_device(first, t)
 
 
 def _no_grad(*ts):
@@ -266,7 +277,7 @@ def _indices(idx: Optional[torch.Tensor], batch: int, slots: int):
 
 # ------------------------------------------------------- short convolution
 def _conv_setup(x, weight, bias, initial_state, cu_seqlens, activation, *more):
-    _one_device(x, weight, bias, initial_state, cu_seqlens, *more)
+    _same_device(x, weight, bias, initial_state, cu_seqlens, *more)
     if x.dim() != 3 or weight.dim() != 2:
         _bad("x must be [B, T, C] and weight [C, W]")
     if activation not in (None, "silu"):
@@ -329,7 +340,7 @@ def short_conv_step(x, state, weight, bias=None, *, state_indices=None, activati
     state_indices (int32 [N]; None: slot n; negative: an unused row, zero output).  Returns
     y [N, C]."""
     _no_grad(x, state, weight, bias)
-    _one_device(x, state, weight, bias, state_indices, dev_status)
+    _same_device(x, state, weight, bias, state_indices, dev_status)
     if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
         _bad("x must be [N, C], weight [C, W] and state [slots, W-1, C]")
     if activation not in (None, "silu"):
@@ -376,7 +387,7 @@ def short_conv_autograd(x, weight, bias=None, *, initial_state=None, cu_seqlens=
 
 # ------------------------------------------------------------------ the scan
 def _ssm_setup(x, dt, A_log, Bm, Cm, D, dt_bias, initial_state, cu_seqlens, dt_softplus, *more):
-    _one_device(x, dt, A_log, Bm, Cm, D, dt_bias, initial_state, cu_seqlens, *more)
+    _same_device(x, dt, A_log, Bm, Cm, D, dt_bias, initial_state, cu_seqlens, *more)
     if x.dim() != 4 or Bm.dim() != 4:
         _bad("x must be [B, T, H, P], Bm and Cm [B, T, G, N]")
     B, T, H, P = x.shape
@@ -464,7 +475,7 @@ def ssm_step(x, dt, A_log, Bm, Cm, state, *, D=None, dt_bias=None, dt_softplus=T
     [slots, H, Ns, P] fp32 is advanced in place at state_indices (int32 [N]; None: slot n;
     negative: an unused row, zero output).  Returns y [N, H, P]."""
     _no_grad(x, dt, A_log, Bm, Cm, D, dt_bias, state)
-    _one_device(x, dt, A_log, Bm, Cm, D, dt_bias, state, state_indices, dev_status)
+    _same_device(x, dt, A_log, Bm, Cm, D, dt_bias, state, state_indices, dev_status)
     if x.dim() != 3 or Bm.dim() != 3 or state.dim() != 4:
         _bad("x must be [N, H, P], Bm and Cm [N, G, Ns], state [slots, H, Ns, P]")
     R, H, P = x.shape
@@ -535,7 +546,7 @@ def add_rms_norm(x, weight, *, residual=None, eps=1e-6, stream=None):
     """h = x + residual and y = h weight / sqrt(mean(h^2) + eps) over the last dimension:
     returns (y, h), both in x's type (h is x itself without a residual)."""
     _no_grad(x, weight, residual)
-    _one_device(x, weight, residual)
+    _same_device(x, weight, residual)
     x = x.contiguous()
     shape, weight = _norm_setup(x, weight, eps)
     residual = _want("residual", residual, x.shape, x.dtype)
@@ -551,7 +562,7 @@ def add_rms_norm_quant(x, weight, *, residual=None, eps=1e-6, out_dtype="e4m3", 
     x's shape and scale [..., groups] fp32, one per row (group 0) or per 128 columns (group
     128): q * scale stands for the normalised row."""
     _no_grad(x, weight, residual)
-    _one_device(x, weight, residual)
+    _same_device(x, weight, residual)
     kinds = {"e4m3": (KDA_NORM_E4M3, torch.float8_e4m3fn), "int8": (KDA_NORM_INT8, torch.int8)}
     if out_dtype not in kinds:
         _bad(f"out_dtype {out_dtype!r} (supported: 'e4m3', 'int8')")
@@ -572,7 +583,7 @@ def add_rms_norm_backward(dy, h, weight, *, eps=1e-6, dresidual=None, workspace=
     """The gradients of add_rms_norm at its returned h, for dy and the residual stream's own
     gradient (or None): a dict of dx (x's and the residual's alike) and dweight (fp32)."""
     dy, h, weight = dy.detach(), h.detach().contiguous(), weight.detach()
-    _one_device(dy, h, weight, dresidual, workspace)
+    _same_device(dy, h, weight, dresidual, workspace)
     shape, weight = _norm_setup(h, weight, eps)
     dy = _want("dy", dy, h.shape, h.dtype)
     dresidual = _want("dresidual", dresidual, h.shape, h.dtype)

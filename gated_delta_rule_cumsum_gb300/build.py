@@ -34,6 +34,8 @@ SOURCES = [
     "kda_conv.cu",
     "kda_norm.cu",
     "kda_ssm.cu",
+    "kda_ssm_tc.cu",
+    "kda_ssm_tc_bwd.cu",
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -74,22 +74,42 @@ struct SsmArgs {
     ChunkCtrl *ctrl;
     int32_t *chunk_start;          // [N + 1] (packed only)
     int64_t slots;
-    float *states;                 // [slots][H][Ns][P]: the state at each chunk's start
+    float *states;                 // per (slot, head) ssm_state_bytes: the state at each chunk's
+                                   // start ([Ns][P] fp32, or the tensor-core path's tiles)
+    void *rows;                    // per (slot, head) ssm_rows_bytes: the rows' decays
     float *decay;                  // [slots][H]: each chunk's decay from start to end
     // backward
     const void *dy;
     const float *dht;
     void *dx, *ddt, *dB, *dC;
     float *dA_log, *dD, *ddt_bias, *dh0;
-    float *dstates;                // [slots][H][Ns][P]: the state gradient at each chunk's end
-    float *dBh, *dCh;              // [rows][H][Ns]: the heads' shares of dB and dC
+    float *dstates;                // the state gradient at each chunk's end, as states
+    // fp32 path: the heads' shares of dB and dC ([rows][H][Ns]); tensor-core path: those of the
+    // parts a group's heads are split in ([slots][G][parts][128][Ns])
+    float *dBh, *dCh;
+    int parts;
     float *sums;                   // [slots][3][H]: the chunks' shares of dA_log, dD, ddt_bias
+    // tensor-core path, per (slot, head, 64-column tile): what the rows' decay gradients are
+    // made of (4 x 128), and dD; per (slot, head) the shares of <E, S>
+    float *rowg, *dDp, *es;
 };
 int ssm_chunk_len(kda_dtype dt, int Ns, int P);
 cudaError_t launch_ssm_fwd(const SsmArgs &a, kda_dtype dt, cudaStream_t st);
 // The chunk states alone (the first part of the forward).
 cudaError_t launch_ssm_states(const SsmArgs &a, kda_dtype dt, cudaStream_t st);
 cudaError_t launch_ssm_bwd(const SsmArgs &a, kda_dtype dt, cudaStream_t st);
+// The tensor-core path (kda_ssm_tc.cu): bf16, Ns a multiple of 8 up to 128, P of 8.
+bool ssm_tc_supported(kda_dtype dt, int Ns, int P);
+size_t ssm_state_bytes(kda_dtype dt, int Ns, int P);
+size_t ssm_rows_bytes(kda_dtype dt, int Ns, int P);
+cudaError_t launch_ssm_tc_states(const SsmArgs &a, cudaStream_t st);
+cudaError_t launch_ssm_tc_dstates(const SsmArgs &a, cudaStream_t st);
+cudaError_t launch_ssm_tc_out(const SsmArgs &a, cudaStream_t st);
+cudaError_t launch_ssm_tc_bwd(const SsmArgs &a, cudaStream_t st);
+// The parts a group's units are split in for dB and dC; the bytes of the arrays above.
+int ssm_tc_parts(int64_t slots, int G, int units);
+int ssm_tc_tiles(int P);
+size_t ssm_tc_es_floats(int Ns, int P);
 
 struct SsmStepArgs {
     const void *x, *dt, *Bm, *Cm;

@@ -89,7 +89,7 @@ kda_status check_conv(const char *op, const kda_conv_shape *s, const int32_t *cu
 }
 
 struct SsmWs {
-    size_t ctrl, chunk_start, decay, states, total;
+    size_t ctrl, chunk_start, decay, rows, states, total;
 };
 int64_t ssm_slots(const kda_ssm_shape *s, bool packed, int L) {
     const int64_t per = ((int64_t)s->T + L - 1) / L;
@@ -105,23 +105,31 @@ SsmWs ssm_ws(const kda_ssm_shape *s) {
     w.ctrl = 0;
     w.chunk_start = 256;
     w.decay = w.chunk_start + kda::align_up(sizeof(int32_t) * ((size_t)s->num_seqs + 1), 256);
-    w.states = kda::align_up(w.decay + (size_t)slots * s->H * 4, 256);
-    w.total = kda::align_up(w.states + (size_t)slots * s->H * s->N * s->P * 4, 256);
+    w.rows = kda::align_up(w.decay + (size_t)slots * s->H * 4, 256);
+    w.states = kda::align_up(w.rows + (size_t)slots * s->H * kda::ssm_rows_bytes(s->dtype, s->N, s->P), 256);
+    w.total = kda::align_up(w.states + (size_t)slots * s->H * kda::ssm_state_bytes(s->dtype, s->N, s->P), 256);
     return w;
 }
 struct SsmBwdWs {
-    size_t dstates, dBh, dCh, sums, fwd, total;
+    size_t dstates, dBh, dCh, sums, rowg, dDp, es, fwd, total;
+    int parts;
 };
 SsmBwdWs ssm_bwd_ws(const kda_ssm_shape *s, bool saved) {
     SsmBwdWs w;
     const int L = kda::ssm_chunk_len(s->dtype, s->N, s->P);
-    const size_t slots = (size_t)ssm_slots(s, may_be_packed(s), L);
-    const size_t share = (size_t)s->B * s->T * s->H * s->N * 4;
+    const bool tc = kda::ssm_tc_supported(s->dtype, s->N, s->P);
+    const size_t slots = (size_t)ssm_slots(s, may_be_packed(s), L), heads = slots * s->H;
+    const size_t tiles = tc ? kda::ssm_tc_tiles(s->P) : 0;
+    w.parts = tc ? kda::ssm_tc_parts((int64_t)slots, s->G, (int)(s->H / s->G * tiles)) : 1;
+    const size_t share = tc ? slots * s->G * w.parts * L * s->N * 4 : (size_t)s->B * s->T * s->H * s->N * 4;
     w.dstates = 0;
-    w.dBh = kda::align_up(slots * s->H * s->N * s->P * 4, 256);
+    w.dBh = kda::align_up(heads * kda::ssm_state_bytes(s->dtype, s->N, s->P), 256);
     w.dCh = kda::align_up(w.dBh + share, 256);
     w.sums = kda::align_up(w.dCh + share, 256);
-    w.fwd = kda::align_up(w.sums + slots * 3 * s->H * 4, 256);
+    w.rowg = kda::align_up(w.sums + heads * 3 * 4, 256);
+    w.dDp = kda::align_up(w.rowg + heads * tiles * 4 * L * 4, 256);
+    w.es = kda::align_up(w.dDp + heads * tiles * 4, 256);
+    w.fwd = kda::align_up(w.es + (tc ? heads * kda::ssm_tc_es_floats(s->N, s->P) * 4 : 0), 256);
     w.total = w.fwd + (saved ? 0 : ssm_ws(s).total);
     return w;
 }
@@ -164,6 +172,7 @@ void carve_fwd(const kda_ssm_shape *s, char *ws, kda::SsmArgs *a) {
     a->ctrl = reinterpret_cast<kda::ChunkCtrl *>(ws + w.ctrl);
     a->chunk_start = reinterpret_cast<int32_t *>(ws + w.chunk_start);
     a->decay = reinterpret_cast<float *>(ws + w.decay);
+    a->rows = ws + w.rows;
     a->states = reinterpret_cast<float *>(ws + w.states);
 }
 
@@ -310,12 +319,18 @@ kda_status kda_ssm_scan_bwd(const void *x, const void *dt, const float *A_log, c
     a.dBh = reinterpret_cast<float *>(ws + w.dBh);
     a.dCh = reinterpret_cast<float *>(ws + w.dCh);
     a.sums = reinterpret_cast<float *>(ws + w.sums);
+    a.rowg = reinterpret_cast<float *>(ws + w.rowg);
+    a.dDp = reinterpret_cast<float *>(ws + w.dDp);
+    a.es = reinterpret_cast<float *>(ws + w.es);
+    a.parts = w.parts;
     cudaStream_t s = to_stream(stream);
     cudaError_t e = cudaSuccess;
     if (cu_seqlens && rows > 0) {
         const size_t es = shape->dtype == KDA_DTYPE_BF16 ? 2 : 4;
         e = cudaMemsetAsync(dx, 0, (size_t)rows * a.H * a.P * es, s);
         if (e == cudaSuccess) e = cudaMemsetAsync(ddt, 0, (size_t)rows * a.H * es, s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, (size_t)rows * a.G * a.Ns * es, s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dC, 0, (size_t)rows * a.G * a.Ns * es, s);
         if (e != cudaSuccess) return done(e, op);
     }
     if (saved) {  // read only: the forward's stores

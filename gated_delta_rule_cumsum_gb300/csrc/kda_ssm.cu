@@ -297,7 +297,22 @@ __global__ void __launch_bounds__(256) ssm_chunk_out_kernel(SsmArgs p) {
     load_tile<false>(Sx, static_cast<const T *>(p.x) + c.r0 * p.x_stride + (int64_t)h * p.P + p0, p.x_stride,
                      c.nr, pcols, nullptr);
     __syncthreads();
+    float inter[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) inter[i][j] = y[i][j];
     mm64(y, Ct, Sx);
+    // a non-finite x_s reaches rows r < s through 0 x_s: such rows are summed again up to r
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (!isfinite(y[i][j])) {
+                y[i][j] = inter[i][j];
+                for (int s = 0; s <= 4 * ty + i; ++s)
+                    y[i][j] = fmaf(Ct[s * kLD + 4 * ty + i], Sx[s * kLD + 4 * tx + j], y[i][j]);
+            }
     const float D = p.D ? p.D[h] : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -784,6 +799,13 @@ cudaError_t fwd(const SsmArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+cudaError_t param_sums(const SsmArgs &a, cudaStream_t st) {
+    prof_begin("ssm_param_sum", st);
+    ssm_param_sum_kernel<<<(unsigned)((3 * a.H + 3) / 4), 128, 0, st>>>(a);
+    prof_end(st);
+    return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t bwd(const SsmArgs &a, cudaStream_t st) {
     cudaError_t e = ssm_setup<T>();
@@ -804,23 +826,41 @@ cudaError_t bwd(const SsmArgs &a, cudaStream_t st) {
         prof_end(st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    prof_begin("ssm_param_sum", st);
-    ssm_param_sum_kernel<<<(unsigned)((3 * a.H + 3) / 4), 128, 0, st>>>(a);
-    prof_end(st);
-    return cudaGetLastError();
+    return param_sums(a, st);
 }
 
 }  // namespace
 
-int ssm_chunk_len(kda_dtype, int, int) { return kL; }
+int ssm_chunk_len(kda_dtype dt, int Ns, int P) { return ssm_tc_supported(dt, Ns, P) ? 128 : kL; }
+
+namespace {
+cudaError_t tc_states(const SsmArgs &a, cudaStream_t st) {
+    if (a.cu) {
+        const cudaError_t e =
+            launch_validate_offsets(a.cu, a.N, a.T, a.status, a.ctrl, a.chunk_start, st, a.L);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_ssm_tc_states(a, st);
+}
+}  // namespace
 
 cudaError_t launch_ssm_states(const SsmArgs &a, kda_dtype dt, cudaStream_t st) {
+    if (ssm_tc_supported(dt, a.Ns, a.P)) return tc_states(a, st);
     return dt == KDA_DTYPE_BF16 ? states<__nv_bfloat16>(a, st) : states<float>(a, st);
 }
 cudaError_t launch_ssm_fwd(const SsmArgs &a, kda_dtype dt, cudaStream_t st) {
+    if (ssm_tc_supported(dt, a.Ns, a.P)) {
+        const cudaError_t e = tc_states(a, st);
+        return e != cudaSuccess ? e : launch_ssm_tc_out(a, st);
+    }
     return dt == KDA_DTYPE_BF16 ? fwd<__nv_bfloat16>(a, st) : fwd<float>(a, st);
 }
 cudaError_t launch_ssm_bwd(const SsmArgs &a, kda_dtype dt, cudaStream_t st) {
+    if (ssm_tc_supported(dt, a.Ns, a.P)) {
+        cudaError_t e = launch_ssm_tc_dstates(a, st);
+        if (e == cudaSuccess) e = launch_ssm_tc_bwd(a, st);
+        return e == cudaSuccess ? param_sums(a, st) : e;
+    }
     return dt == KDA_DTYPE_BF16 ? bwd<__nv_bfloat16>(a, st) : bwd<float>(a, st);
 }
 
