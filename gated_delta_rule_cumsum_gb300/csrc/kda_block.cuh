@@ -23,8 +23,7 @@ struct ConvArgs {
     int strip;                     // rows a thread walks
     int64_t strips;                // over all B * T rows
 };
-// Rows per strip: chosen so that a call has enough threads to hide memory latency.
-int conv_strip(int B, int T, int C, int vec);
+// Rows per strip of the backward (its workspace holds one row of sums per strip).
 int conv_bwd_strip(int B, int T, int C);
 cudaError_t launch_conv_fwd(ConvArgs a, kda_dtype dt, cudaStream_t st);
 cudaError_t launch_conv_bwd(ConvArgs a, kda_dtype dt, cudaStream_t st);

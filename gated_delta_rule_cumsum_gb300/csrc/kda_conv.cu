@@ -9,6 +9,8 @@
 // A thread owns a few adjacent channels and walks down a strip of rows with the last
 // W - 1 rows in registers, so each row is read once (and W - 1 rows more per strip, from
 // L2).  All arithmetic is fp32; outputs are rounded once.
+#include <type_traits>
+
 #include "kda_block.cuh"
 
 namespace kda {
@@ -18,10 +20,12 @@ constexpr int kConvThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ float sigmoid_of(float x) {
-    if constexpr (sizeof(T) == 4)
-        return 1.f / (1.f + expf(-x));
-    else  // the fast exponential and division: about 2^-21, far inside the output's rounding
-        return __fdividef(1.f, 1.f + __expf(-x));
+    if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-x));
+    // the approximate exponential and reciprocal, one special-function operation each: a
+    // relative error near 2^-22, far inside a bf16 output's rounding
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_ftz(-1.4426950408889634f * x)));
+    return r;
 }
 
 // The sequence that row t (of all B * T rows) belongs to: its index, first row and end.
@@ -42,16 +46,72 @@ __device__ __forceinline__ bool find_seq(const ConvArgs &p, int64_t t, int &n, i
     return true;
 }
 
-template <typename T, int VEC, int W, bool AL>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
-    const int cblocks = (p.C + VEC * kConvThreads - 1) / (VEC * kConvThreads);
-    const int64_t strip = blockIdx.x / cblocks;
-    const int c = ((int)(blockIdx.x % cblocks) * kConvThreads + threadIdx.x) * VEC;
-    if (p.cu && blockIdx.x == 0) check_offsets(p.cu, p.N, p.T, p.status);
-    if (c >= p.C) return;
-    const int nc = min(VEC, p.C - c);
-    const T *x = static_cast<const T *>(p.x) + c;
+// A thread's four channels.  Vector loads want them adjacent; where rows are not aligned for
+// those, they lie 32 apart, so that each scalar load of a warp is still one line.
+constexpr int kCh = 4;
+template <typename T, bool AL>
+struct Channels {
+    int c, C;
+    __device__ __forceinline__ Channels(int block, int C_) : C(C_) {
+        const int base = block * kCh * kConvThreads;
+        c = AL ? base + (int)threadIdx.x * kCh
+               : base + ((int)threadIdx.x >> 5) * 32 * kCh + ((int)threadIdx.x & 31);
+    }
+    __device__ __forceinline__ int at(int j) const { return AL ? c + j : c + 32 * j; }
+    __device__ __forceinline__ bool in(int j) const { return at(j) < C; }
+    // raw: as it lies in memory, converted where it is used
+    using Raw = typename std::conditional<sizeof(T) == 4, float4, uint2>::type;
+    __device__ __forceinline__ Raw load(const T *row) const {
+        Raw r{};
+        if constexpr (AL) {
+            r = *reinterpret_cast<const Raw *>(row + c);
+        } else {
+            T *e = reinterpret_cast<T *>(&r);
+#pragma unroll
+            for (int j = 0; j < kCh; ++j)
+                if (in(j)) e[j] = row[at(j)];
+        }
+        return r;
+    }
+    static __device__ __forceinline__ void widen(const Raw &r, float (&v)[kCh]) {
+        load_vec<T, kCh, true>(reinterpret_cast<const T *>(&r), kCh, v);
+    }
+    __device__ __forceinline__ void load(const T *row, float (&v)[kCh]) const { widen(load(row), v); }
+    __device__ __forceinline__ void store(T *row, const float (&v)[kCh]) const {
+        if constexpr (AL) {
+            store_vec<T, kCh, true>(row + c, kCh, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kCh; ++j)
+                if (in(j)) row[at(j)] = from_f32<T>(v[j]);
+        }
+    }
+};
+
+// The row r of a sequence that starts at s: of x, or of the carried state before it, or zero.
+template <typename T, bool AL>
+__device__ __forceinline__ void row_or_state(const ConvArgs &p, const Channels<T, AL> &ch, int W, int n,
+                                             int64_t s, int64_t r, float (&v)[kCh]) {
     const T *st = static_cast<const T *>(p.state_in);
+#pragma unroll
+    for (int j = 0; j < kCh; ++j) v[j] = 0.f;
+    if (r >= s)
+        ch.load(static_cast<const T *>(p.x) + r * p.x_stride, v);
+    else if (st)
+        ch.load(st + ((int64_t)n * (W - 1) + (W - 1) + (r - s)) * p.C, v);
+}
+
+// U rows at a time: while a group is worked on, the next one's loads are on their way.
+template <typename T, int W, bool AL>
+__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
+    constexpr int U = 4;
+    using Ch = Channels<T, AL>;
+    const int cblocks = (p.C + kCh * kConvThreads - 1) / (kCh * kConvThreads);
+    const int64_t strip = blockIdx.x / cblocks;
+    const Ch ch((int)(blockIdx.x % cblocks), p.C);
+    if (p.cu && blockIdx.x == 0) check_offsets(p.cu, p.N, p.T, p.status);
+    if (!ch.in(0)) return;
+    const T *x = static_cast<const T *>(p.x);
 
     if (strip >= p.strips) {  // the final state of one sequence: its last W - 1 rows
         const int n = (int)(strip - p.strips);
@@ -63,75 +123,78 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
             s = (int64_t)n * p.T;
             e = s + p.T;
         }
-        T *out = static_cast<T *>(p.state_out) + (int64_t)n * (W - 1) * p.C + c;
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
-            const int64_t r = e - (W - 1) + k;
-            float v[VEC] = {};
-            if (r >= s)
-                load_vec<T, VEC, AL>(x + r * p.x_stride, nc, v);
-            else if (st)
-                load_vec<T, VEC, AL>(st + ((int64_t)n * (W - 1) + (W - 1) + (r - s)) * p.C + c, nc, v);
-            store_vec<T, VEC, AL>(out + (int64_t)k * p.C, nc, v);
+            float v[kCh];
+            row_or_state<T, AL>(p, ch, W, n, s, e - (W - 1) + k, v);
+            ch.store(static_cast<T *>(p.state_out) + ((int64_t)n * (W - 1) + k) * p.C, v);
         }
         return;
     }
 
-    float w[W][VEC], bias[VEC];
+    float w[W][kCh], bias[kCh];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const bool in = j < nc;
-        bias[j] = in && p.bias ? p.bias[c + j] : 0.f;
+    for (int j = 0; j < kCh; ++j) {
+        bias[j] = ch.in(j) && p.bias ? p.bias[ch.at(j)] : 0.f;
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k][j] = in ? p.w[(int64_t)(c + j) * W + k] : 0.f;
+        for (int k = 0; k < W; ++k) w[k][j] = ch.in(j) ? p.w[(int64_t)ch.at(j) * W + k] : 0.f;
     }
-    T *y = static_cast<T *>(p.y) + c;
-    constexpr int U = 4;  // rows loaded ahead of their arithmetic
+    T *y = static_cast<T *>(p.y);
     const int64_t t1 = min((strip + 1) * (int64_t)p.strip, (int64_t)p.B * p.T);
     for (int64_t t = strip * p.strip; t < t1;) {
         int n;
         int64_t s, e;
         if (!find_seq(p, t, n, s, e)) return;
         e = min(e, t1);
-        float win[W - 1 + U][VEC];
+        const int rows = (int)(e - t);
+        const T *px = x + t * p.x_stride;
+        T *py = y + t * p.C;
+        float win[W - 1 + U][kCh];
+        typename Ch::Raw raw[U];
+        if (rows >= U)
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) {
-            const int64_t r = t - (W - 1) + k;
+            for (int u = 0; u < U; ++u) raw[u] = ch.load(px + u * p.x_stride);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) win[k][j] = 0.f;
-            if (r >= s)
-                load_vec<T, VEC, AL>(x + r * p.x_stride, nc, win[k]);
-            else if (st)
-                load_vec<T, VEC, AL>(st + ((int64_t)n * (W - 1) + (W - 1) + (r - s)) * p.C + c, nc,
-                                     win[k]);
-        }
-        for (; t < e; t += U) {
-            const int rows = (int)min((int64_t)U, e - t);
+        for (int k = 0; k < W - 1; ++k) row_or_state<T, AL>(p, ch, W, n, s, t - (W - 1) + k, win[k]);
+        auto out = [&](int u, T *row) {  // from rows u .. u + W - 1 of the window
+            float o[kCh];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (u < rows) load_vec<T, VEC, AL>(x + (t + u) * p.x_stride, nc, win[W - 1 + u]);
+            for (int j = 0; j < kCh; ++j) {
+                float a = bias[j];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u >= rows) break;
-                float o[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    float a = bias[j];
-#pragma unroll
-                    for (int k = 0; k < W; ++k) a = fmaf(w[k][j], win[u + k][j], a);
-                    o[j] = p.silu ? a * sigmoid_of<T>(a) : a;
-                }
-                store_vec<T, VEC, AL>(y + (t + u) * p.C, nc, o);
+                for (int k = 0; k < W; ++k) a = fmaf(w[k][j], win[u + k][j], a);
+                o[j] = p.silu ? a * sigmoid_of<T>(a) : a;
             }
-            if (rows < U) {  // the sequence or the strip ends inside this group
-                t += rows;
-                break;
-            }
+            ch.store(row, o);
+        };
+        int left = rows;
+        for (; left >= U; left -= U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) Ch::widen(raw[u], win[W - 1 + u]);
+            px += U * p.x_stride;
+            if (left >= 2 * U)
+#pragma unroll
+                for (int u = 0; u < U; ++u) raw[u] = ch.load(px + u * p.x_stride);
+#pragma unroll
+            for (int u = 0; u < U; ++u) out(u, py + (int64_t)u * p.C);
+            py += (int64_t)U * p.C;
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) win[k][j] = win[U + k][j];
+                for (int j = 0; j < kCh; ++j) win[k][j] = win[U + k][j];
         }
+#pragma unroll 1
+        for (; left > 0; --left) {
+            ch.load(px, win[W - 1]);
+            out(0, py);
+            px += p.x_stride;
+            py += p.C;
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) win[k][j] = win[k + 1][j];
+        }
+        t = e;
     }
 }
 
@@ -142,30 +205,27 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
 // t .. t + W - 1; the row that enters is u = t + W - 1.  dw and dbias take the rows of
 // the strip alone; each strip leaves its sums in p.part and a second kernel adds the
 // strips in order, so that no result depends on the order of atomics.
-template <typename T, int VEC, int W, bool AL>
+template <typename T, int W, bool AL>
 __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs p) {
-    const int cblocks = (p.C + VEC * kConvThreads - 1) / (VEC * kConvThreads);
+    constexpr int U = 4;
+    using Ch = Channels<T, AL>;
+    const int cblocks = (p.C + kCh * kConvThreads - 1) / (kCh * kConvThreads);
     const int64_t strip = blockIdx.x / cblocks;
-    const int c = ((int)(blockIdx.x % cblocks) * kConvThreads + threadIdx.x) * VEC;
+    const Ch ch((int)(blockIdx.x % cblocks), p.C);
     if (p.cu && blockIdx.x == 0) check_offsets(p.cu, p.N, p.T, p.status);
-    if (c >= p.C) return;
-    const int nc = min(VEC, p.C - c);
-    const T *x = static_cast<const T *>(p.x) + c;
-    const T *dy = static_cast<const T *>(p.dy) + c;
-    const T *st = static_cast<const T *>(p.state_in);
+    if (!ch.in(0)) return;
+    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
     const T *dso = static_cast<const T *>(p.dstate_out);
-    T *dx = static_cast<T *>(p.dx) + c;
-    T *dsi = static_cast<T *>(p.dstate_in);
+    T *dx = static_cast<T *>(p.dx), *dsi = static_cast<T *>(p.dstate_in);
 
-    float w[W][VEC], bias[VEC], dw[W][VEC], db[VEC];
+    float w[W][kCh], bias[kCh], dw[W][kCh], db[kCh];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        const bool in = j < nc;
-        bias[j] = in && p.bias ? p.bias[c + j] : 0.f;
+    for (int j = 0; j < kCh; ++j) {
+        bias[j] = ch.in(j) && p.bias ? p.bias[ch.at(j)] : 0.f;
         db[j] = 0.f;
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-            w[k][j] = in ? p.w[(int64_t)(c + j) * W + k] : 0.f;
+            w[k][j] = ch.in(j) ? p.w[(int64_t)ch.at(j) * W + k] : 0.f;
             dw[k][j] = 0.f;
         }
     }
@@ -175,91 +235,128 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs p) {
         int64_t s, e;
         if (!find_seq(p, t, n, s, e)) break;
         const int64_t end = min(e, t1);
-        float xw[W][VEC] = {}, dp[W][VEC] = {};
+        // windows of a group of positions pos .. pos + U - 1: rows pos .. pos + W - 2 + U
+        float xw[W - 1 + U][kCh], dp[W - 1 + U][kCh];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) {  // rows t - (W - 1) .. t - 1
-            const int64_t r = t - (W - 1) + k;
-            if (r >= s)
-                load_vec<T, VEC, AL>(x + r * p.x_stride, nc, xw[k + 1]);
-            else if (st)
-                load_vec<T, VEC, AL>(st + ((int64_t)n * (W - 1) + (W - 1) + (r - s)) * p.C + c, nc,
-                                     xw[k + 1]);
+        for (int k = 0; k < W - 1; ++k) {
+            row_or_state<T, AL>(p, ch, W, n, s, t - (W - 1) + k, xw[k]);
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) dp[k][j] = 0.f;
         }
-        // xw[k] holds row pos + k once the entering row is in; before it, shifted by one
-        constexpr int U = 4;
-        for (int64_t pos0 = t - (W - 1); pos0 < end; pos0 += U) {
-            float xn[U][VEC], gn[U][VEC];
+        // dp of the entering row at window place q, from dy; and its share of dw, dbias
+        auto enter = [&](int q, bool own) {
+            if (p.silu) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int64_t u = pos0 + i + W - 1;
+                for (int j = 0; j < kCh; ++j) {
+                    float a = bias[j];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) xn[i][j] = gn[i][j] = 0.f;
-                if (u < e && pos0 + i < end) {
-                    load_vec<T, VEC, AL>(x + u * p.x_stride, nc, xn[i]);
-                    load_vec<T, VEC, AL>(dy + u * p.C, nc, gn[i]);
+                    for (int k = 0; k < W; ++k) a = fmaf(w[k][j], xw[q - (W - 1) + k][j], a);
+                    const float sg = sigmoid_of<T>(a);
+                    dp[q][j] *= sg * fmaf(a, 1.f - sg, 1.f);
                 }
             }
+            if (own) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int64_t pos = pos0 + i, u = pos + W - 1;
-                if (pos >= end) break;
+                for (int j = 0; j < kCh; ++j) {
+                    db[j] += dp[q][j];
 #pragma unroll
-                for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        xw[k][j] = xw[k + 1][j];
-                        dp[k][j] = dp[k + 1][j];
-                    }
-                const bool own = u >= t && u < end;
-                float o[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    xw[W - 1][j] = xn[i][j];
-                    float g = gn[i][j];
-                    if (p.silu) {
-                        float a = bias[j];
-#pragma unroll
-                        for (int k = 0; k < W; ++k) a = fmaf(w[k][j], xw[k][j], a);
-                        const float sg = sigmoid_of<T>(a);
-                        // a select: a row past the sequence has g = 0 whatever sigmoid gives
-                        g = u < e ? g * (sg * (1.f + a * (1.f - sg))) : 0.f;
-                    }
-                    dp[W - 1][j] = g;
-                    if (own) {
-                        db[j] += g;
-#pragma unroll
-                        for (int k = 0; k < W; ++k) dw[k][j] = fmaf(g, xw[k][j], dw[k][j]);
-                    }
-                    float d = 0.f;
-#pragma unroll
-                    for (int m = 0; m < W; ++m) d = fmaf(w[W - 1 - m][j], dp[m][j], d);
-                    o[j] = d;
-                }
-                const bool state_row = pos < s;
-                if (state_row ? (dsi != nullptr && t == s) : pos >= t) {
-                    const int64_t k = pos - (e - (W - 1));  // its row of the final state
-                    if (dso && k >= 0) {
-                        float f[VEC];
-                        load_vec<T, VEC, AL>(dso + ((int64_t)n * (W - 1) + k) * p.C + c, nc, f);
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) o[j] += f[j];
-                    }
-                    T *dst = state_row
-                                 ? dsi + ((int64_t)n * (W - 1) + (W - 1) + (pos - s)) * p.C + c
-                                 : dx + pos * p.C;
-                    store_vec<T, VEC, AL>(dst, nc, o);
+                    for (int k = 0; k < W; ++k) dw[k][j] = fmaf(dp[q][j], xw[q - (W - 1) + k][j], dw[k][j]);
                 }
             }
+        };
+        auto leave = [&](int q, float (&o)[kCh]) {  // dx of window place q
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) {
+                o[j] = 0.f;
+#pragma unroll
+                for (int m = 0; m < W; ++m) o[j] = fmaf(w[W - 1 - m][j], dp[q + m][j], o[j]);
+            }
+        };
+        auto move = [&](int by) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    xw[k][j] = xw[by + k][j];
+                    dp[k][j] = dp[by + k][j];
+                }
+        };
+        // one position with every check: the first and last ones, where rows of the state or of
+        // the next strip take part
+        auto step = [&](int64_t pos) {
+            const int64_t u = pos + W - 1;
+#pragma unroll
+            for (int j = 0; j < kCh; ++j) xw[W - 1][j] = dp[W - 1][j] = 0.f;
+            if (u < e) {  // (a row past the sequence adds nothing whatever sigmoid would give)
+                ch.load(x + u * p.x_stride, xw[W - 1]);
+                ch.load(dy + u * p.C, dp[W - 1]);
+                enter(W - 1, u < end);
+            }
+            const bool state_row = pos < s;
+            if (state_row ? dsi != nullptr && t == s : pos >= t) {
+                float o[kCh];
+                leave(0, o);
+                const int64_t k = pos - (e - (W - 1));  // its row of the final state
+                if (dso && k >= 0) {
+                    float f[kCh];
+                    ch.load(dso + ((int64_t)n * (W - 1) + k) * p.C, f);
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) o[j] += f[j];
+                }
+                ch.store(state_row ? dsi + ((int64_t)n * (W - 1) + (W - 1) + (pos - s)) * p.C : dx + pos * p.C, o);
+            }
+            move(1);
+        };
+        int64_t pos = t - (W - 1);
+#pragma unroll 1
+        for (; pos < min(t, end); ++pos) step(pos);
+        // positions whose entering row is the strip's own
+        int left = (int)(end - (W - 1) - pos);
+        if (left >= U) {
+            const T *px = x + (pos + W - 1) * p.x_stride, *pg = dy + (pos + W - 1) * p.C;
+            T *po = dx + pos * p.C;
+            typename Ch::Raw xn[U], gn[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                xn[i] = ch.load(px + i * p.x_stride);
+                gn[i] = ch.load(pg + (int64_t)i * p.C);
+            }
+            for (; left >= U; left -= U, pos += U) {
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    Ch::widen(xn[i], xw[W - 1 + i]);
+                    Ch::widen(gn[i], dp[W - 1 + i]);
+                }
+                px += U * p.x_stride;
+                pg += (int64_t)U * p.C;
+                if (left >= 2 * U)
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        xn[i] = ch.load(px + i * p.x_stride);
+                        gn[i] = ch.load(pg + (int64_t)i * p.C);
+                    }
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    enter(W - 1 + i, true);
+                    float o[kCh];
+                    leave(i, o);
+                    ch.store(po + (int64_t)i * p.C, o);
+                }
+                po += (int64_t)U * p.C;
+                move(U);
+            }
         }
+#pragma unroll 1
+        for (; pos < end; ++pos) step(pos);
         t = end;
     }
-    float *part = p.part + strip * (int64_t)(W + 1) * p.C + c;
+    float *part = p.part + strip * (int64_t)(W + 1) * p.C;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
-        if (j < nc) {
+    for (int j = 0; j < kCh; ++j)
+        if (ch.in(j)) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) part[(int64_t)k * p.C + j] = dw[k][j];
-            part[(int64_t)W * p.C + j] = db[j];
+            for (int k = 0; k < W; ++k) part[(int64_t)k * p.C + ch.at(j)] = dw[k][j];
+            part[(int64_t)W * p.C + ch.at(j)] = db[j];
         }
 }
 
@@ -298,34 +395,33 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, in
     }
 }
 
-template <typename T, int VEC, int W, bool AL>
+template <typename T, int W, bool AL>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepArgs p) {
-    const int cblocks = (p.C + VEC * kConvThreads - 1) / (VEC * kConvThreads);
+    using Ch = Channels<T, AL>;
+    const int cblocks = (p.C + kCh * kConvThreads - 1) / (kCh * kConvThreads);
     const int n = blockIdx.x / cblocks;
-    const int c = ((int)(blockIdx.x % cblocks) * kConvThreads + threadIdx.x) * VEC;
+    const Ch ch((int)(blockIdx.x % cblocks), p.C);
     const int slot = state_slot(p.idx, n, p.slots, p.status);
-    if (c >= p.C) return;
-    const int nc = min(VEC, p.C - c);
-    T *y = static_cast<T *>(p.y) + (int64_t)n * p.C + c;
-    float o[VEC] = {};
+    if (!ch.in(0)) return;
+    float o[kCh] = {};
     if (slot >= 0) {
-        T *st = static_cast<T *>(p.state) + (int64_t)slot * (W - 1) * p.C + c;
-        float win[W][VEC];
+        T *st = static_cast<T *>(p.state) + (int64_t)slot * (W - 1) * p.C;
+        float win[W][kCh];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) load_vec<T, VEC, AL>(st + (int64_t)k * p.C, nc, win[k]);
-        load_vec<T, VEC, AL>(static_cast<const T *>(p.x) + (int64_t)n * p.x_stride + c, nc, win[W - 1]);
+        for (int k = 0; k < W - 1; ++k) ch.load(st + (int64_t)k * p.C, win[k]);
+        ch.load(static_cast<const T *>(p.x) + (int64_t)n * p.x_stride, win[W - 1]);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const int cj = c + min(j, nc - 1);
-            float a = p.bias ? p.bias[cj] : 0.f;
+        for (int j = 0; j < kCh; ++j) {
+            const int c = min(ch.at(j), p.C - 1);
+            float a = p.bias ? p.bias[c] : 0.f;
 #pragma unroll
-            for (int k = 0; k < W; ++k) a = fmaf(p.w[(int64_t)cj * W + k], win[k][j], a);
+            for (int k = 0; k < W; ++k) a = fmaf(p.w[(int64_t)c * W + k], win[k][j], a);
             o[j] = p.silu ? a * sigmoid_of<T>(a) : a;
         }
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) store_vec<T, VEC, AL>(st + (int64_t)k * p.C, nc, win[k + 1]);
+        for (int k = 0; k < W - 1; ++k) ch.store(st + (int64_t)k * p.C, win[k + 1]);
     }
-    store_vec<T, VEC, AL>(y, nc, o);
+    ch.store(static_cast<T *>(p.y) + (int64_t)n * p.C, o);
 }
 
 // Whether every row of the given tensors starts on a `bytes` boundary.
@@ -347,48 +443,48 @@ cudaError_t by_width(int W, F &&f) {
     return cudaGetLastError();
 }
 
-int strip_for(int64_t rows, int64_t threads_per_row, int most) {
+int strip_for(int64_t rows, int C, int most) {
+    const int64_t per_row = (C + kCh - 1) / kCh;
     int strip = most;
-    while (strip > 8 && (rows + strip - 1) / strip * threads_per_row < 152 * 1024) strip /= 2;
+    while (strip > 8 && (rows + strip - 1) / strip * per_row < 152 * 1024) strip /= 2;
     return strip;
 }
 
+// f(type, taps, aligned)
+template <typename F>
+cudaError_t by_kind(kda_dtype dt, int W, bool al, F &&f) {
+    using std::integral_constant;
+    return by_width(W, [&](auto taps) {
+        if (dt == KDA_DTYPE_BF16) {
+            if (al) f(__nv_bfloat16(), taps, integral_constant<bool, true>());
+            else f(__nv_bfloat16(), taps, integral_constant<bool, false>());
+        } else {
+            if (al) f(float(), taps, integral_constant<bool, true>());
+            else f(float(), taps, integral_constant<bool, false>());
+        }
+    });
+}
+int64_t channel_blocks(int C) { return (C + kCh * kConvThreads - 1) / (kCh * kConvThreads); }
+
 }  // namespace
 
-// 64 rows where that still gives 152 x 1024 threads (half of what the GPU holds): a strip
-// re-reads W - 1 rows, 5% of its traffic at 64; fewer rows where the input is short.
-int conv_strip(int B, int T, int C, int vec) {
-    return strip_for((int64_t)B * T, (C + vec - 1) / vec, 64);
-}
-int conv_bwd_strip(int B, int T, int C) {
-    return strip_for((int64_t)B * T, (C + 3) / 4, 128);
-}
+// Long strips re-read little (W - 1 rows each) and leave few partial sums; short inputs get
+// shorter ones, down to 8 rows, until there are 152 x 1024 threads.
+int conv_bwd_strip(int B, int T, int C) { return strip_for((int64_t)B * T, C, 128); }
 
 cudaError_t launch_conv_fwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {
     const size_t e = dt == KDA_DTYPE_BF16 ? 2 : 4;
     const void *ptrs[] = {a.x, a.y, a.state_in, a.state_out};
-    const bool al = rows_aligned(ptrs, 4, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), 16);
-    const int vec = dt == KDA_DTYPE_BF16 && al ? 8 : 4;
-    a.strip = conv_strip(a.B, a.T, a.C, vec);
+    const bool al = rows_aligned(ptrs, 4, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), kCh * e);
     const int64_t rows = (int64_t)a.B * a.T;
+    a.strip = strip_for(rows, a.C, 64);
     a.strips = (rows + a.strip - 1) / a.strip;
-    const int64_t cblocks = (a.C + vec * kConvThreads - 1) / (vec * kConvThreads);
-    const int64_t blocks = cblocks * (a.strips + (a.state_out ? a.N : 0));
+    const int64_t blocks = channel_blocks(a.C) * (a.strips + (a.state_out ? a.N : 0));
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     prof_begin("conv_fwd", st);
-    const cudaError_t err = by_width(a.W, [&](auto W) {
-        const unsigned g = (unsigned)blocks;
-        if (dt == KDA_DTYPE_BF16) {
-            if (al)
-                conv_fwd_kernel<__nv_bfloat16, 8, W(), true><<<g, kConvThreads, 0, st>>>(a);
-            else
-                conv_fwd_kernel<__nv_bfloat16, 4, W(), false><<<g, kConvThreads, 0, st>>>(a);
-        } else if (al) {
-            conv_fwd_kernel<float, 4, W(), true><<<g, kConvThreads, 0, st>>>(a);
-        } else {
-            conv_fwd_kernel<float, 4, W(), false><<<g, kConvThreads, 0, st>>>(a);
-        }
+    const cudaError_t err = by_kind(dt, a.W, al, [&](auto t, auto W, auto AL) {
+        conv_fwd_kernel<decltype(t), W(), AL()><<<(unsigned)blocks, kConvThreads, 0, st>>>(a);
     });
     prof_end(st);
     return err;
@@ -397,28 +493,17 @@ cudaError_t launch_conv_fwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {
 cudaError_t launch_conv_bwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {
     const size_t e = dt == KDA_DTYPE_BF16 ? 2 : 4;
     const void *ptrs[] = {a.x, a.dy, a.dx, a.state_in, a.dstate_out, a.dstate_in};
-    const bool al = rows_aligned(ptrs, 6, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), 4 * e);
+    const bool al = rows_aligned(ptrs, 6, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), kCh * e);
     a.strip = conv_bwd_strip(a.B, a.T, a.C);
     const int64_t rows = (int64_t)a.B * a.T;
     a.strips = (rows + a.strip - 1) / a.strip;
-    const int64_t cblocks = (a.C + 4 * kConvThreads - 1) / (4 * kConvThreads);
-    const int64_t blocks = cblocks * a.strips;
+    const int64_t blocks = channel_blocks(a.C) * a.strips;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaError_t err = cudaSuccess;
     if (blocks > 0) {
         prof_begin("conv_bwd", st);
-        err = by_width(a.W, [&](auto W) {
-            const unsigned g = (unsigned)blocks;
-            if (dt == KDA_DTYPE_BF16) {
-                if (al)
-                    conv_bwd_kernel<__nv_bfloat16, 4, W(), true><<<g, kConvThreads, 0, st>>>(a);
-                else
-                    conv_bwd_kernel<__nv_bfloat16, 4, W(), false><<<g, kConvThreads, 0, st>>>(a);
-            } else if (al) {
-                conv_bwd_kernel<float, 4, W(), true><<<g, kConvThreads, 0, st>>>(a);
-            } else {
-                conv_bwd_kernel<float, 4, W(), false><<<g, kConvThreads, 0, st>>>(a);
-            }
+        err = by_kind(dt, a.W, al, [&](auto t, auto W, auto AL) {
+            conv_bwd_kernel<decltype(t), W(), AL()><<<(unsigned)blocks, kConvThreads, 0, st>>>(a);
         });
         prof_end(st);
         if (err != cudaSuccess) return err;
@@ -443,23 +528,13 @@ cudaError_t launch_conv_bwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {
 cudaError_t launch_conv_step(const ConvStepArgs &a, kda_dtype dt, cudaStream_t st) {
     const size_t e = dt == KDA_DTYPE_BF16 ? 2 : 4;
     const void *ptrs[] = {a.x, a.y, a.state};
-    const bool al = rows_aligned(ptrs, 3, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), 4 * e);
-    const int64_t blocks = (int64_t)a.N * ((a.C + 4 * kConvThreads - 1) / (4 * kConvThreads));
+    const bool al = rows_aligned(ptrs, 3, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), kCh * e);
+    const int64_t blocks = (int64_t)a.N * channel_blocks(a.C);
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     prof_begin("conv_step", st);
-    const cudaError_t err = by_width(a.W, [&](auto W) {
-        const unsigned g = (unsigned)blocks;
-        if (dt == KDA_DTYPE_BF16) {
-            if (al)
-                conv_step_kernel<__nv_bfloat16, 4, W(), true><<<g, kConvThreads, 0, st>>>(a);
-            else
-                conv_step_kernel<__nv_bfloat16, 4, W(), false><<<g, kConvThreads, 0, st>>>(a);
-        } else if (al) {
-            conv_step_kernel<float, 4, W(), true><<<g, kConvThreads, 0, st>>>(a);
-        } else {
-            conv_step_kernel<float, 4, W(), false><<<g, kConvThreads, 0, st>>>(a);
-        }
+    const cudaError_t err = by_kind(dt, a.W, al, [&](auto t, auto W, auto AL) {
+        conv_step_kernel<decltype(t), W(), AL()><<<(unsigned)blocks, kConvThreads, 0, st>>>(a);
     });
     prof_end(st);
     return err;

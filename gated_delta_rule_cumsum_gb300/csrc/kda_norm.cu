@@ -80,104 +80,122 @@ __device__ __forceinline__ void store_q(uint8_t *p, int n, const float (&v)[VEC]
     }
 }
 
+// VEC columns as they lie in memory: loaded for the next row while this one is worked on.
+template <typename T, int VEC, bool AL>
+struct Vec {
+    T v[VEC];
+    __device__ __forceinline__ void load(const T *p, int n) {
+        if constexpr (AL) {
+            constexpr int B = VEC * (int)sizeof(T);
+            if constexpr (B == 16)
+                *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
+            else
+                *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[j] = j < n ? p[j] : from_f32<T>(0.f);
+        }
+    }
+    __device__ __forceinline__ float at(int j) const { return to_f32(v[j]); }
+};
+constexpr int blocks_per_sm(int maxt) { return maxt <= 256 ? 4 : 1; }
+
 // NV vectors of VEC columns per thread: thread i of a row holds vectors i, i + tpr, ...
 // Eight (bf16) or four (fp32) adjacent columns per thread make a 128-column scale group
-// 16 or 32 adjacent lanes of one warp.
+// 16 or 32 adjacent lanes of one warp.  A grid that fills the GPU once walks over the rows:
+// the weights stay in registers, and a row's loads are issued while the row before it is
+// summed and stored.
 template <typename T, int VEC, int NV, bool AL, bool Q, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormArgs p, int tpr) {
+__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT)) norm_fwd_kernel(NormArgs p, int tpr) {
     __shared__ float red[32];
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-    const int tid = threadIdx.x % tpr;
-    const bool live = row < p.rows;
-    const T *x = static_cast<const T *>(p.x) + row * p.cols;
-    const T *res = static_cast<const T *>(p.res) + row * p.cols;
-    T *h = static_cast<T *>(p.h) + row * p.cols;
-
-    float v[NV][VEC];
-    float ss[1] = {0.f};
+    const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
+    const int64_t first = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr, step = (int64_t)gridDim.x * rpb;
+    // every thread makes the same number of rounds: the sums have block-wide barriers
+    const int64_t rounds = (p.rows + step - 1) / step;
+    float w[NV][VEC];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) v[i][j] = 0.f;
-        if (live && n > 0) load_vec<T, VEC, AL>(x + c, n, v[i]);
-    }
-    if (p.res) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-            float r[VEC];
-            if (live && n > 0) {
-                load_vec<T, VEC, AL>(res + c, n, r);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) v[i][j] += r[j];
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
-        if (live && n > 0 && p.h) store_vec<T, VEC, AL>(h + c, n, v[i]);
-    }
-    row_sum<1>(ss, tpr, red);
-    const float rstd = 1.f / sqrtf(ss[0] / (float)p.cols + p.eps);
-
-    float amax = 0.f;
-    float gmax[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-        float w[VEC] = {};
-        if (n > 0) {
-            if constexpr (AL) {
-#pragma unroll
-                for (int j = 0; j < VEC; j += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(p.w + c + j);
-                    w[j] = f.x; w[j + 1] = f.y; w[j + 2] = f.z; w[j + 3] = f.w;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) w[j] = j < n ? p.w[c + j] : 0.f;
-            }
-        }
-        gmax[i] = 0.f;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            v[i][j] = v[i][j] * rstd * w[j];
-            if (Q) gmax[i] = fmaxf(gmax[i], fabsf(v[i][j]));
+            const int c = (tid + i * tpr) * VEC + j;
+            w[i][j] = c < p.cols ? p.w[c] : 0.f;
         }
-        if constexpr (!Q) {
-            if (live && n > 0)
-                store_vec<T, VEC, AL>(static_cast<T *>(p.y) + row * p.cols + c, n, v[i]);
-        } else {
-            amax = fmaxf(amax, gmax[i]);
-        }
-    }
-    if constexpr (Q) {
-        const float top = p.out == KDA_NORM_E4M3 ? 448.f : 127.f;
-        uint8_t *q = static_cast<uint8_t *>(p.y) + row * p.cols;
-        if (p.group == 0) amax = row_max(amax, tpr, red);
-        const int groups = p.group ? (p.cols + 127) / 128 : 1;
+    Vec<T, VEC, AL> xn[NV], rn[NV];
+    auto fetch = [&](int64_t row) {
+        const T *x = static_cast<const T *>(p.x) + row * p.cols, *r = static_cast<const T *>(p.res) + row * p.cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-            float m = amax;
-            if (p.group) {
-                m = gmax[i];
-#pragma unroll
-                for (int o = 64 / VEC; o > 0; o >>= 1)
-                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (row < p.rows && n > 0) {
+                xn[i].load(x + c, n);
+                if (p.res) rn[i].load(r + c, n);
             }
-            const float scale = m > 0.f ? m / top : 1.f;
-            const float inv = 1.f / scale;
-            if (live && n > 0) {
-                if (p.group ? c % 128 == 0 : c == 0)
-                    p.scale[row * groups + (p.group ? c / 128 : 0)] = scale;
+        }
+    };
+    fetch(first);
+    const int groups = p.group ? (p.cols + 127) / 128 : 1;
+    for (int64_t k = 0; k < rounds; ++k) {
+        const int64_t row = first + k * step;
+        const bool live = row < p.rows;
+        float v[NV][VEC], ss[1] = {0.f};
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) v[i][j] *= inv;
-                store_q<VEC, AL>(q + c, n, v[i], p.out);
+        for (int i = 0; i < NV; ++i) {
+            const int c = (tid + i * tpr) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                const bool in = live && c + (AL ? 0 : j) < p.cols;
+                v[i][j] = in ? (p.res ? xn[i].at(j) + rn[i].at(j) : xn[i].at(j)) : 0.f;
+                ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+            }
+        }
+        if (k + 1 < rounds) fetch(row + step);
+        if (p.h) {
+            T *h = static_cast<T *>(p.h) + row * p.cols;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+                if (live && n > 0) store_vec<T, VEC, AL>(h + c, n, v[i]);
+            }
+        }
+        row_sum<1>(ss, tpr, red);
+        const float rstd = 1.f / sqrtf(ss[0] / (float)p.cols + p.eps);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                v[i][j] = v[i][j] * rstd * w[i][j];
+                if (Q) amax = fmaxf(amax, fabsf(v[i][j]));
+            }
+            if constexpr (!Q)
+                if (live && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.y) + row * p.cols + c, n, v[i]);
+        }
+        if constexpr (Q) {
+            const float top = p.out == KDA_NORM_E4M3 ? 448.f : 127.f;
+            uint8_t *q = static_cast<uint8_t *>(p.y) + row * p.cols;
+            if (p.group == 0) amax = row_max(amax, tpr, red);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+                float m = amax;
+                if (p.group) {
+                    m = 0.f;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) m = fmaxf(m, fabsf(v[i][j]));
+#pragma unroll
+                    for (int o = 64 / VEC; o > 0; o >>= 1)
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                }
+                const float scale = m > 0.f ? m / top : 1.f;
+                const float inv = 1.f / scale;
+                if (live && n > 0) {
+                    if (p.group ? c % 128 == 0 : c == 0)
+                        p.scale[row * groups + (p.group ? c / 128 : 0)] = scale;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) v[i][j] *= inv;
+                    store_q<VEC, AL>(q + c, n, v[i], p.out);
+                }
             }
         }
     }
@@ -185,11 +203,11 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(NormArgs p, int tpr) {
 
 // Gradients at the stored h:  with g = dy w, xhat = h rstd,
 //     dx = rstd (g - xhat mean(g xhat)) + dres,    dw = sum over rows of dy xhat.
-// Both row sums (h^2 and g h) come from one exchange.  A block walks over rows, one row per
-// tpr threads at a time; a thread keeps its columns' share of dw in registers and leaves it
-// in p.part, and a second kernel adds the shares in a fixed order.
+// Both row sums (h^2 and g h) come from one exchange.  The grid walks over the rows as the
+// forward's does; a thread keeps its columns' share of dw in registers and leaves it in p.part,
+// and a second kernel adds the shares in a fixed order.
 template <typename T, int VEC, int NV, bool AL, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormArgs p, int tpr) {
+__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT)) norm_bwd_kernel(NormArgs p, int tpr) {
     __shared__ float red[64];
     const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
     float dw[NV][VEC] = {}, w[NV][VEC];
@@ -199,34 +217,41 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormArgs p, int tpr) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) w[i][j] = j < n ? p.w[c + j] : 0.f;
     }
-    const int64_t lane_row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-    const int64_t step = (int64_t)gridDim.x * rpb;
-    // every thread makes the same number of rounds: the sums have block-wide barriers
+    const int64_t first = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr, step = (int64_t)gridDim.x * rpb;
     const int64_t rounds = (p.rows + step - 1) / step;
-    for (int64_t k = 0; k < rounds; ++k) {
-        const int64_t row = lane_row + k * step;
-        const bool live = row < p.rows;
+    Vec<T, VEC, AL> hn[NV], gn[NV], rn[NV];
+    auto fetch = [&](int64_t row) {
         const int64_t at = row * p.cols;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            if (row < p.rows && n > 0) {
+                hn[i].load(static_cast<const T *>(p.h) + at + c, n);
+                gn[i].load(static_cast<const T *>(p.dy) + at + c, n);
+                if (p.dres) rn[i].load(static_cast<const T *>(p.dres) + at + c, n);
+            }
+        }
+    };
+    fetch(first);
+    for (int64_t k = 0; k < rounds; ++k) {
+        const int64_t row = first + k * step, at = row * p.cols;
+        const bool live = row < p.rows;
         float h[NV][VEC], g[NV][VEC], r[NV][VEC];
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) h[i][j] = g[i][j] = r[i][j] = 0.f;
-            if (live && n > 0) {
-                load_vec<T, VEC, AL>(static_cast<const T *>(p.h) + at + c, n, h[i]);
-                load_vec<T, VEC, AL>(static_cast<const T *>(p.dy) + at + c, n, g[i]);
-                if (p.dres) load_vec<T, VEC, AL>(static_cast<const T *>(p.dres) + at + c, n, r[i]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
+            const int c = (tid + i * tpr) * VEC;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
+                const bool in = live && c + (AL ? 0 : j) < p.cols;
+                h[i][j] = in ? hn[i].at(j) : 0.f;
+                g[i][j] = in ? gn[i].at(j) : 0.f;
+                r[i][j] = in && p.dres ? rn[i].at(j) : 0.f;
                 s[0] = fmaf(h[i][j], h[i][j], s[0]);
                 s[1] = fmaf(g[i][j] * w[i][j], h[i][j], s[1]);
             }
+        }
+        if (k + 1 < rounds) fetch(row + step);
         row_sum<2>(s, tpr, red);
         const float rstd = 1.f / sqrtf(s[0] / (float)p.cols + p.eps);
         const float m = s[1] / (float)p.cols * rstd;  // mean(g xhat)
@@ -243,7 +268,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(NormArgs p, int tpr) {
             if (live && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.dx) + at + c, n, o);
         }
     }
-    float *part = p.part + lane_row * p.cols;
+    float *part = p.part + first * p.cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (tid + i * tpr) * VEC;
@@ -310,11 +335,11 @@ void by_plan(const RowPlan &r, F &&f) {
         f(std::integral_constant<int, 4>(), std::integral_constant<int, 256>());
 }
 
-// Blocks of the backward: enough for every SM to hold its fill of threads, at most one
-// per row; each leaves one row of partial sums per row it works on at a time.
-int64_t bwd_blocks(int64_t rows, const RowPlan &r) {
-    const int64_t want = 152 * (int64_t)(1024 / (r.tpr * r.rpb) > 0 ? 1024 / (r.tpr * r.rpb) : 1);
-    const int64_t most = (rows + r.rpb - 1) / r.rpb;
+// Blocks of either direction: what the GPU's 152 SMs hold at once, at most one per row (the
+// backward leaves one row of partial sums per row that a block works on at a time).
+int64_t row_blocks(int64_t rows, const RowPlan &r) {
+    const int threads = r.tpr * r.rpb, per_sm = threads > 256 ? 1 : 1024 / threads;
+    const int64_t want = 152 * (int64_t)per_sm, most = (rows + r.rpb - 1) / r.rpb;
     return want < most ? want : most;
 }
 
@@ -322,7 +347,7 @@ int64_t bwd_blocks(int64_t rows, const RowPlan &r) {
 
 int64_t norm_bwd_parts(int64_t rows, int cols) {
     const RowPlan r = row_plan((cols + 3) / 4);
-    return r.tpr == 0 ? 0 : bwd_blocks(rows, r) * r.rpb;
+    return r.tpr == 0 ? 0 : row_blocks(rows, r) * r.rpb;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
@@ -332,8 +357,8 @@ cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
     const bool al = norm_aligned(a, bf ? 2 : 4, ptrs, 4);
     const int vec = bf ? 8 : 4;
     const RowPlan r = row_plan((a.cols + vec - 1) / vec);
-    const int64_t blocks = (a.rows + r.rpb - 1) / r.rpb;
-    if (r.tpr == 0 || blocks > INT32_MAX) return cudaErrorInvalidValue;
+    if (r.tpr == 0) return cudaErrorInvalidValue;
+    const int64_t blocks = row_blocks(a.rows, r);
     prof_begin("norm_fwd", st);
     by_plan(r, [&](auto NV, auto MAXT) {
         const unsigned g = (unsigned)blocks, t = (unsigned)(r.tpr * r.rpb);
@@ -368,7 +393,7 @@ cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
     for (const void *q : ptrs) al = al && aligned_to(q, bf ? 8 : 16);
     const RowPlan r = row_plan((a.cols + 3) / 4);
     if (r.tpr == 0) return cudaErrorInvalidValue;
-    const int64_t blocks = bwd_blocks(a.rows, r);
+    const int64_t blocks = row_blocks(a.rows, r);
     if (blocks > 0) {
         prof_begin("norm_bwd", st);
         by_plan(r, [&](auto NV, auto MAXT) {
