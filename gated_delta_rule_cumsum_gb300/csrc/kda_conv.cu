@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
 // the strip alone; each strip leaves its sums in p.part and a second kernel adds the
 // strips in order, so that no result depends on the order of atomics.
 template <typename T, int W, bool AL>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs p) {
+__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 2 ? 4 : 3) conv_bwd_kernel(ConvArgs p) {
     constexpr int U = 4;
     using Ch = Channels<T, AL>;
     const int cblocks = (p.C + kCh * kConvThreads - 1) / (kCh * kConvThreads);
@@ -395,33 +395,62 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, in
     }
 }
 
+// One token per row.  A thread takes `per` batch rows, four at a time, so that its channels'
+// weights (twice the bytes of a row's state) are read once for all of them.
+constexpr int kStepRows = 4;
 template <typename T, int W, bool AL>
-__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepArgs p) {
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepArgs p, int per) {
     using Ch = Channels<T, AL>;
     const int cblocks = (p.C + kCh * kConvThreads - 1) / (kCh * kConvThreads);
-    const int n = blockIdx.x / cblocks;
+    const int n0 = (int)(blockIdx.x / cblocks) * per, n1 = min(n0 + per, p.N);
     const Ch ch((int)(blockIdx.x % cblocks), p.C);
-    const int slot = state_slot(p.idx, n, p.slots, p.status);
+    if (blockIdx.x % cblocks == 0)
+        for (int n = n0 + threadIdx.x; n < n1; n += kConvThreads)
+            if (p.idx && p.idx[n] >= p.slots) report(p.status, KDA_DEVICE_BAD_INDEX);
     if (!ch.in(0)) return;
-    float o[kCh] = {};
-    if (slot >= 0) {
-        T *st = static_cast<T *>(p.state) + (int64_t)slot * (W - 1) * p.C;
-        float win[W][kCh];
+    float w[W][kCh], bias[kCh];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) ch.load(st + (int64_t)k * p.C, win[k]);
-        ch.load(static_cast<const T *>(p.x) + (int64_t)n * p.x_stride, win[W - 1]);
+    for (int j = 0; j < kCh; ++j) {
+        const int c = min(ch.at(j), p.C - 1);
+        bias[j] = p.bias ? p.bias[c] : 0.f;
 #pragma unroll
-        for (int j = 0; j < kCh; ++j) {
-            const int c = min(ch.at(j), p.C - 1);
-            float a = p.bias ? p.bias[c] : 0.f;
+        for (int k = 0; k < W; ++k) w[k][j] = p.w[(int64_t)c * W + k];
+    }
+    for (int n = n0; n < n1; n += kStepRows) {
+        typename Ch::Raw raw[kStepRows][W];
+        T *st[kStepRows];
 #pragma unroll
-            for (int k = 0; k < W; ++k) a = fmaf(p.w[(int64_t)c * W + k], win[k][j], a);
-            o[j] = p.silu ? a * sigmoid_of<T>(a) : a;
+        for (int r = 0; r < kStepRows; ++r) {
+            st[r] = nullptr;
+            if (n + r >= n1) continue;
+            const int slot = p.idx ? p.idx[n + r] : n + r;
+            if (slot < 0 || slot >= p.slots) continue;  // an unused row, or a reported one
+            st[r] = static_cast<T *>(p.state) + (int64_t)slot * (W - 1) * p.C;
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) raw[r][k] = ch.load(st[r] + (int64_t)k * p.C);
+            raw[r][W - 1] = ch.load(static_cast<const T *>(p.x) + (int64_t)(n + r) * p.x_stride);
         }
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) ch.store(st + (int64_t)k * p.C, win[k + 1]);
+        for (int r = 0; r < kStepRows; ++r) {
+            if (n + r >= n1) break;
+            float o[kCh] = {};
+            if (st[r]) {
+                float win[W][kCh];
+#pragma unroll
+                for (int k = 0; k < W; ++k) Ch::widen(raw[r][k], win[k]);
+#pragma unroll
+                for (int j = 0; j < kCh; ++j) {
+                    float a = bias[j];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) a = fmaf(w[k][j], win[k][j], a);
+                    o[j] = p.silu ? a * sigmoid_of<T>(a) : a;
+                }
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) ch.store(st[r] + (int64_t)k * p.C, win[k + 1]);
+            }
+            ch.store(static_cast<T *>(p.y) + (int64_t)(n + r) * p.C, o);
+        }
     }
-    ch.store(static_cast<T *>(p.y) + (int64_t)n * p.C, o);
 }
 
 // Whether every row of the given tensors starts on a `bytes` boundary.
@@ -529,12 +558,15 @@ cudaError_t launch_conv_step(const ConvStepArgs &a, kda_dtype dt, cudaStream_t s
     const size_t e = dt == KDA_DTYPE_BF16 ? 2 : 4;
     const void *ptrs[] = {a.x, a.y, a.state};
     const bool al = rows_aligned(ptrs, 3, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), kCh * e);
-    const int64_t blocks = (int64_t)a.N * channel_blocks(a.C);
+    // as many rows per thread as leave 8 blocks for every SM
+    const int64_t cb = channel_blocks(a.C), most = (int64_t)a.N * cb / (152 * 8);
+    const int per = most < 1 ? 1 : most > 32 ? 32 : (int)most;
+    const int64_t blocks = (a.N + per - 1) / per * cb;
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     prof_begin("conv_step", st);
     const cudaError_t err = by_kind(dt, a.W, al, [&](auto t, auto W, auto AL) {
-        conv_step_kernel<decltype(t), W(), AL()><<<(unsigned)blocks, kConvThreads, 0, st>>>(a);
+        conv_step_kernel<decltype(t), W(), AL()><<<(unsigned)blocks, kConvThreads, 0, st>>>(a, per);
     });
     prof_end(st);
     return err;

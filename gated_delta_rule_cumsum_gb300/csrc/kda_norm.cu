@@ -98,7 +98,9 @@ struct Vec {
     }
     __device__ __forceinline__ float at(int j) const { return to_f32(v[j]); }
 };
-constexpr int blocks_per_sm(int maxt) { return maxt <= 256 ? 4 : 1; }
+// Blocks that an SM holds: of 256 threads four with one or two vectors per thread (64
+// registers), three in the backward and two with four, which need more of them.
+constexpr int blocks_per_sm(int maxt, int nv, bool bwd) { return maxt > 256 ? 1 : nv == 4 ? 2 : bwd ? 3 : 4; }
 
 // NV vectors of VEC columns per thread: thread i of a row holds vectors i, i + tpr, ...
 // Eight (bf16) or four (fp32) adjacent columns per thread make a 128-column scale group
@@ -106,7 +108,7 @@ constexpr int blocks_per_sm(int maxt) { return maxt <= 256 ? 4 : 1; }
 // the weights stay in registers, and a row's loads are issued while the row before it is
 // summed and stored.
 template <typename T, int VEC, int NV, bool AL, bool Q, int MAXT>
-__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT)) norm_fwd_kernel(NormArgs p, int tpr) {
+__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd_kernel(NormArgs p, int tpr) {
     __shared__ float red[32];
     const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
     const int64_t first = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr, step = (int64_t)gridDim.x * rpb;
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT)) norm_fwd_kernel(Nor
 // forward's does; a thread keeps its columns' share of dw in registers and leaves it in p.part,
 // and a second kernel adds the shares in a fixed order.
 template <typename T, int VEC, int NV, bool AL, int MAXT>
-__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT)) norm_bwd_kernel(NormArgs p, int tpr) {
+__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, true)) norm_bwd_kernel(NormArgs p, int tpr) {
     __shared__ float red[64];
     const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
     float dw[NV][VEC] = {}, w[NV][VEC];
@@ -337,8 +339,9 @@ void by_plan(const RowPlan &r, F &&f) {
 
 // Blocks of either direction: what the GPU's 152 SMs hold at once, at most one per row (the
 // backward leaves one row of partial sums per row that a block works on at a time).
-int64_t row_blocks(int64_t rows, const RowPlan &r) {
-    const int threads = r.tpr * r.rpb, per_sm = threads > 256 ? 1 : 1024 / threads;
+int64_t row_blocks(int64_t rows, const RowPlan &r, bool bwd) {
+    const int threads = r.tpr * r.rpb;
+    const int per_sm = threads > 256 ? 1 : blocks_per_sm(256, r.nv, bwd) * 256 / threads;
     const int64_t want = 152 * (int64_t)per_sm, most = (rows + r.rpb - 1) / r.rpb;
     return want < most ? want : most;
 }
@@ -347,7 +350,7 @@ int64_t row_blocks(int64_t rows, const RowPlan &r) {
 
 int64_t norm_bwd_parts(int64_t rows, int cols) {
     const RowPlan r = row_plan((cols + 3) / 4);
-    return r.tpr == 0 ? 0 : row_blocks(rows, r) * r.rpb;
+    return r.tpr == 0 ? 0 : row_blocks(rows, r, true) * r.rpb;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
@@ -358,7 +361,7 @@ cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
     const int vec = bf ? 8 : 4;
     const RowPlan r = row_plan((a.cols + vec - 1) / vec);
     if (r.tpr == 0) return cudaErrorInvalidValue;
-    const int64_t blocks = row_blocks(a.rows, r);
+    const int64_t blocks = row_blocks(a.rows, r, false);
     prof_begin("norm_fwd", st);
     by_plan(r, [&](auto NV, auto MAXT) {
         const unsigned g = (unsigned)blocks, t = (unsigned)(r.tpr * r.rpb);
@@ -393,7 +396,7 @@ cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
     for (const void *q : ptrs) al = al && aligned_to(q, bf ? 8 : 16);
     const RowPlan r = row_plan((a.cols + 3) / 4);
     if (r.tpr == 0) return cudaErrorInvalidValue;
-    const int64_t blocks = row_blocks(a.rows, r);
+    const int64_t blocks = row_blocks(a.rows, r, true);
     if (blocks > 0) {
         prof_begin("norm_bwd", st);
         by_plan(r, [&](auto NV, auto MAXT) {
