@@ -381,8 +381,10 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, in
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane, total = (int64_t)(W + 1) * C;
     float s = 0.f;
-    if (i < total)
+    if (i < total) {
+#pragma unroll 8
         for (int64_t r = grp; r < strips; r += 8) s += part[r * total + i];
+    }
     red[grp][lane] = s;
     __syncthreads();
     if (grp == 0 && i < total) {

@@ -82,7 +82,7 @@ __device__ __forceinline__ void store_q(uint8_t *p, int n, const float (&v)[VEC]
 
 // VEC columns as they lie in memory: loaded for the next row while this one is worked on.
 template <typename T, int VEC, bool AL>
-struct Vec {
+struct alignas(VEC * sizeof(T)) Vec {
     T v[VEC];
     __device__ __forceinline__ void load(const T *p, int n) {
         if constexpr (AL) {
@@ -96,7 +96,11 @@ struct Vec {
             for (int j = 0; j < VEC; ++j) v[j] = j < n ? p[j] : from_f32<T>(0.f);
         }
     }
-    __device__ __forceinline__ float at(int j) const { return to_f32(v[j]); }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = from_f32<T>(0.f);
+    }
+    __device__ __forceinline__ void widen(float (&f)[VEC]) const { load_vec<T, VEC, true>(v, VEC, f); }
 };
 // Blocks that an SM holds: of 256 threads four with one or two vectors per thread (64
 // registers), three in the backward and two with four, which need more of them.
@@ -128,6 +132,8 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            xn[i].zero();  // rows and columns past the last add nothing
+            rn[i].zero();
             if (row < p.rows && n > 0) {
                 xn[i].load(x + c, n);
                 if (p.res) rn[i].load(r + c, n);
@@ -142,11 +148,12 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd
         float v[NV][VEC], ss[1] = {0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC;
+            float r[VEC];
+            xn[i].widen(v[i]);
+            rn[i].widen(r);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const bool in = live && c + (AL ? 0 : j) < p.cols;
-                v[i][j] = in ? (p.res ? xn[i].at(j) + rn[i].at(j) : xn[i].at(j)) : 0.f;
+                v[i][j] += r[j];
                 ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
             }
         }
@@ -227,6 +234,9 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, true)) norm_bwd_
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            hn[i].zero();
+            gn[i].zero();
+            rn[i].zero();
             if (row < p.rows && n > 0) {
                 hn[i].load(static_cast<const T *>(p.h) + at + c, n);
                 gn[i].load(static_cast<const T *>(p.dy) + at + c, n);
@@ -242,13 +252,11 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, true)) norm_bwd_
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC;
+            hn[i].widen(h[i]);
+            gn[i].widen(g[i]);
+            rn[i].widen(r[i]);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                const bool in = live && c + (AL ? 0 : j) < p.cols;
-                h[i][j] = in ? hn[i].at(j) : 0.f;
-                g[i][j] = in ? gn[i].at(j) : 0.f;
-                r[i][j] = in && p.dres ? rn[i].at(j) : 0.f;
                 s[0] = fmaf(h[i][j], h[i][j], s[0]);
                 s[1] = fmaf(g[i][j] * w[i][j], h[i][j], s[1]);
             }
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, true)) norm_bwd_
             for (int j = 0; j < VEC; ++j) {
                 const float xh = h[i][j] * rstd;
                 dw[i][j] = fmaf(g[i][j], xh, dw[i][j]);
-                o[j] = rstd * (g[i][j] * w[i][j] - xh * m) + r[i][j];
+                o[j] = fmaf(rstd, fmaf(g[i][j], w[i][j], -xh * m), r[i][j]);
             }
             if (live && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.dx) + at + c, n, o);
         }
@@ -280,18 +288,21 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, true)) norm_bwd_
     }
 }
 
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float *part, int64_t parts, int cols,
-                                                           float *dw) {
-    __shared__ float red[8][33];
+// dw: 32 warps to 32 columns, each adding every 32nd share, then their sums in order.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, int64_t parts, int cols,
+                                                            float *dw) {
+    __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
-    if (c < cols)
-        for (int64_t r = grp; r < parts; r += 8) s += part[r * cols + c];
+    if (c < cols) {
+#pragma unroll 8
+        for (int64_t r = grp; r < parts; r += 32) s += part[r * cols + c];
+    }
     red[grp][lane] = s;
     __syncthreads();
     if (grp == 0 && c < cols) {
-        for (int g = 1; g < 8; ++g) s += red[g][lane];
+        for (int g = 1; g < 32; ++g) s += red[g][lane];
         dw[c] = s;
     }
 }
@@ -414,7 +425,7 @@ cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     prof_begin("norm_bwd_sum", st);
-    norm_bwd_sum_kernel<<<(unsigned)((a.cols + 31) / 32), 256, 0, st>>>(a.part, blocks * r.rpb, a.cols,
+    norm_bwd_sum_kernel<<<(unsigned)((a.cols + 31) / 32), 1024, 0, st>>>(a.part, blocks * r.rpb, a.cols,
                                                                         a.dw);
     prof_end(st);
     return cudaGetLastError();
