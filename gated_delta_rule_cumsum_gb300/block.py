@@ -251,6 +251,8 @@ def _same_device(first, *ts):
 
 
 def _no_grad(*ts):
+    if not torch.is_grad_enabled():
+        return
     for t in ts:
         if t is not None and t.requires_grad:
             raise KdaError(KDA_ERR_UNSUPPORTED,

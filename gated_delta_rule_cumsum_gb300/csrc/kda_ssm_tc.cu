@@ -362,32 +362,30 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
     constexpr int U = 4;
     for (int k0 = 0; k0 < nc; k0 += U) {
         float4 own[U][2];
-        float dk[U];
+        uint4 sv[U][2];  // reverse: the states' hi and lo rows
+        float dk[U], es4[U] = {};
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (k0 + u < nc && live) {
                 const int64_t k = REV ? nc - 1 - (k0 + u) : k0 + u;
                 own[u][0] = *reinterpret_cast<const float4 *>(st + k * hop);
                 own[u][1] = *reinterpret_cast<const float4 *>(st + k * hop + tile);
+                if constexpr (REV) {
+                    sv[u][0] = *reinterpret_cast<const uint4 *>(sf + k * hop);
+                    sv[u][1] = *reinterpret_cast<const uint4 *>(sf + k * hop + tile);
+                }
                 dk[u] = dec[k * p.H];
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (k0 + u < nc) {
+            if (k0 + u < nc && live) {
                 const int64_t k = REV ? nc - 1 - (k0 + u) : k0 + u;
                 if constexpr (REV) {
-                    float sum = 0.f;
-                    if (live) {
-                        float sh8[8], sl8[8];
-                        load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(sf + k * hop), 8, sh8);
-                        load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(sf + k * hop + tile), 8, sl8);
+                    float h8[8], l8[8];
+                    load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(&sv[u][0]), 8, h8);
+                    load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(&sv[u][1]), 8, l8);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) sum = fmaf(run[j], sh8[j] + sl8[j], sum);
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if ((threadIdx.x & 31) == 0) es[k * p.H * per * 4] = sum;
-                    if (!live) continue;
+                    for (int j = 0; j < 8; ++j) es4[u] = fmaf(run[j], h8[j] + l8[j], es4[u]);
                 }
                 uint4 hi, lo;
                 split2(run[0], run[1], hi.x, lo.x);
@@ -401,6 +399,16 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) run[j] = fmaf(dk[u], run[j], f[j]);
             }
+        if constexpr (REV) {  // four sums over the warp at once: lane l ends with that of chunk l % 4
+            const int lane = threadIdx.x & 31;
+            const bool up2 = lane & 2, up1 = lane & 1;
+            const float a = (up2 ? es4[2] : es4[0]) + __shfl_xor_sync(0xffffffffu, up2 ? es4[0] : es4[2], 2);
+            const float b = (up2 ? es4[3] : es4[1]) + __shfl_xor_sync(0xffffffffu, up2 ? es4[1] : es4[3], 2);
+            float c = (up1 ? b : a) + __shfl_xor_sync(0xffffffffu, up1 ? a : b, 1);
+#pragma unroll
+            for (int o = 16; o > 2; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if (lane < U && k0 + lane < nc) es[(int64_t)(nc - 1 - (k0 + lane)) * p.H * per * 4] = c;
+        }
     }
     if (to && live) {
         if (vec) {
@@ -418,8 +426,10 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
 //   G = C B^T           both tiles K-major; stays in tensor memory (columns 0 .. 127)
 //   M (columns 128 ..)  from G: each 16 columns become 8 of bf16 hi and 8 of lo pairs, which
 //                       the next product reads from tensor memory as its left operand
-//   E = C (S_hi, S_lo)  C K-major, S MN-major (rows = K)   64 columns, two buffers
-//   I = (M_hi, M_lo) x  x MN-major                         64 columns, two buffers
+//   E = C (S_hi, S_lo)  C from tensor memory (64 columns, once per chunk and group: read from
+//                       shared memory it would be two thirds of the product's traffic there,
+//                       and shared memory is what the products wait for); S MN-major
+//   I = (M_hi, M_lo) x  x MN-major                         E and I: 64 columns each
 // Sixteen warps bring x, two units ahead, and form M (warp w: rows 32 (w % 4) .., every fourth
 // block of 16 columns); eight form y; one issues the products and the bulk copies of states
 // and decays, two units ahead.  A unit's M and its product I follow one another; E of the next
@@ -435,7 +445,7 @@ struct OutSmem {
     int bad[8][kPT], any_bad[8];   // of the last units' x: per column the first row not finite
     // A wait on a phase's parity has to happen before the next phase but one is over: a barrier
     // has as many copies as its waiters may be rounds apart.
-    uint64_t full[4], x_free[4], i_done[2], e_free[2], m_ready, e_done, cb_ready, g_done;
+    uint64_t full[4], x_free[4], i_done[2], e_free, m_ready, e_done, cb_ready, g_done;
     uint32_t slot_addr;
     int dead;
 };
@@ -464,38 +474,35 @@ __device__ __forceinline__ void drop_non_finite(uint8_t *x, int row, int c8, int
     }
 }
 
-// 16 columns of M from the same of G: rows i, columns 16 J ...
+// 16 columns of M from the same of G: row i, columns 16 J ...  Pairs of columns go through the
+// packed fp32 operations, two to an instruction.
 __device__ __forceinline__ void m_block(const RowDecays &r, int i, int quad, int J, float ai, float li,
                                         const uint32_t (&gram)[16], uint32_t (&o)[16]) {
-    float v[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(gram[q]);
     if (J < 2 * quad) {
         const int e = J * kSub + kSub - 1;
         const float to_ref = ex2_ftz((ai - r.a[e]) + (li - r.lo[e]));
+        const uint64_t ref2 = pack2(to_ref, to_ref);
 #pragma unroll
-        for (int q = 0; q < 16; q += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(&r.fd[J * kSub + q]);
-            v[q] *= to_ref * f.x;
-            v[q + 1] *= to_ref * f.y;
-            v[q + 2] *= to_ref * f.z;
-            v[q + 3] *= to_ref * f.w;
+        for (int q = 0; q < 8; ++q) {
+            const uint64_t f = *reinterpret_cast<const uint64_t *>(&r.fd[J * kSub + 2 * q]);
+            split2p(mul2(pack2(gram[2 * q], gram[2 * q + 1]), mul2(ref2, f)), o[q], o[8 + q]);
         }
     } else {
+        const uint64_t a2 = pack2(ai, ai), l2 = pack2(li, li);
 #pragma unroll
-        for (int q = 0; q < 16; q += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(&r.a[J * kSub + q]);
-            const float4 l = *reinterpret_cast<const float4 *>(&r.lo[J * kSub + q]);
-            const float4 d = *reinterpret_cast<const float4 *>(&r.d[J * kSub + q]);
-            const int j = J * kSub + q;
-            v[q] = j <= i ? v[q] * (ex2_ftz((ai - a.x) + (li - l.x)) * d.x) : 0.f;
-            v[q + 1] = j + 1 <= i ? v[q + 1] * (ex2_ftz((ai - a.y) + (li - l.y)) * d.y) : 0.f;
-            v[q + 2] = j + 2 <= i ? v[q + 2] * (ex2_ftz((ai - a.z) + (li - l.z)) * d.z) : 0.f;
-            v[q + 3] = j + 3 <= i ? v[q + 3] * (ex2_ftz((ai - a.w) + (li - l.w)) * d.w) : 0.f;
+        for (int q = 0; q < 8; ++q) {
+            const int j = J * kSub + 2 * q;
+            const uint64_t a = *reinterpret_cast<const uint64_t *>(&r.a[j]);
+            const uint64_t l = *reinterpret_cast<const uint64_t *>(&r.lo[j]);
+            const uint64_t d = *reinterpret_cast<const uint64_t *>(&r.d[j]);
+            float x, y;
+            unpack2(add2(sub2(a2, a), sub2(l2, l)), x, y);
+            unpack2(mul2(pack2(gram[2 * q], gram[2 * q + 1]), mul2(pack2(ex2_ftz(x), ex2_ftz(y)), d)), x, y);
+            x = j <= i ? x : 0.f;  // a select: above the diagonal the exponential may overflow
+            y = j + 1 <= i ? y : 0.f;
+            split2(x, y, o[q], o[8 + q]);
         }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) split2(v[2 * q], v[2 * q + 1], o[q], o[8 + q]);
 }
 
 template <bool AL, int NK>
@@ -518,8 +525,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
         for (int k = 0; k < 4; ++k) tc::mbar_init(&s.x_free[k], kYWarps);
         for (int k = 0; k < 2; ++k) {
             tc::mbar_init(&s.i_done[k], 1);
-            tc::mbar_init(&s.e_free[k], kYWarps);
         }
+        tc::mbar_init(&s.e_free, kYWarps);
         tc::mbar_init(&s.m_ready, kRowWarps);
         tc::mbar_init(&s.e_done, 1);
         tc::mbar_init(&s.cb_ready, kRowWarps);
@@ -529,7 +536,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
     }
     tc::fence_async_smem();
     const uint32_t tm = tmem_open(&s.slot_addr, 512);
-    const uint32_t G = tm, M = tm + 128, EI = tm + 256;  // EI: two of (E, I)
+    const uint32_t G = tm, M = tm + 128, E = tm + 256, I = tm + 320, CT = tm + 384;
     volatile int *dead = &s.dead;
     auto warp_arrive = [&](uint64_t *bar) {  // one arrival per warp
         __syncwarp();
@@ -575,14 +582,16 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
                     }
                 }
                 ok = ok && wait_or_die(&s.full[it & 3], (it >> 2) & 1, dead, p.status);
-                if (it > 1) ok = ok && wait_or_die(&s.e_free[it & 1], ((it - 2) >> 1) & 1, dead, p.status);
+                if (it > 0) ok = ok && wait_or_die(&s.e_free, (it - 1) & 1, dead, p.status);
                 tc::tc_fence_after();
                 if (ok) {
-                    const uint32_t E = EI + (it & 1) * 128;
-                    const uint64_t sd = tc::sdesc(tc::smem_addr(s.S[it & 1]), kPT * 16, 128);
+                    uint64_t sd = tc::sdesc(tc::smem_addr(s.S[it & 1]), kPT * 16, 128);
 #pragma unroll 1
-                    for (int q = 0; q < 2; ++q)
-                        mma_steps(E, c_desc, 16, sd + q * (NK * kPT * 2 / 16), 2 * kPT, id_e, NK / 16, q);
+                    for (int k = 0; k < NK / 16; ++k) {
+                        mma_bf16_ts(E, CT + 8 * k, sd, id_e, k > 0);
+                        mma_bf16_ts(E, CT + 8 * k, sd + NK * kPT * 2 / 16, id_e, 1);
+                        sd += 2 * kPT;
+                    }
                     tc::mma_commit(&s.e_done);
                 }
             };
@@ -593,7 +602,6 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
                 const bool ok = wait_or_die(&s.m_ready, it & 1, dead, p.status);
                 tc::tc_fence_after();
                 if (ok) {
-                    const uint32_t I = EI + (it & 1) * 128 + 64;
                     uint64_t xd = tc::sdesc(tc::smem_addr(s.x[it & 3]), kPT * 16, 128);
 #pragma unroll 1
                     for (int k = 0; k < kTL / 16; ++k) {
@@ -672,6 +680,17 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
                                                 p.b_stride, w.c.nr, p.Ns);
                 cp_async_wait_all();
                 tc::fence_async_smem();
+                bar_sync(5, kRowThreads);
+                if (part < NK / 32) {  // 32 columns of C's rows, in pairs
+                    uint32_t o[16];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(&o[4 * q]) = *reinterpret_cast<const uint4 *>(
+                            s.C + (i >> 3) * (NK * 16) + (part * 4 + q) * 128 + (i & 7) * 16);
+                    tmem_st16_nowait(tc::tmem_at(CT, quad * 32, part * 16), o);
+                    tmem_wait_st();
+                    tc::tc_fence_before();
+                }
                 warp_arrive(&s.cb_ready);
                 at_slot = w.slot;
                 at_g = w.g;
@@ -702,11 +721,12 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
             if (it > 0) w.next(p, true);
             wait_or_die(&s.full[it & 3], (it >> 2) & 1, dead, p.status);
             const float ea = ex2_ftz(s.dec[it & 3].a[i]), D = p.D ? p.D[w.h] : 0.f;
+            const uint64_t ea2 = pack2(ea, ea), D2 = pack2(D, D);
             wait_or_die(&s.i_done[it & 1], (it >> 1) & 1, dead, p.status);
             tc::tc_fence_after();
             const uint8_t *x = s.x[it & 3] + (i >> 3) * (kPT * 16) + (i & 7) * 16;
             const bool any_bad = s.any_bad[it & 7] != 0;
-            const uint32_t at = tc::tmem_at(EI + (it & 1) * 128, quad * 32, half * 32);
+            const uint32_t at = tc::tmem_at(E, quad * 32, half * 32);
 #pragma unroll 1
             for (int k = 0; k < 2; ++k) {
                 uint32_t e[16], u[16];
@@ -715,7 +735,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
                 tmem_wait_ld();
                 if (k == 1) {
                     tc::tc_fence_before();
-                    warp_arrive(&s.e_free[it & 1]);
+                    warp_arrive(&s.e_free);
                 }
                 const int c16 = half * 4 + k * 2;  // 16-byte columns c16, c16 + 1
                 if (any_bad) {
@@ -725,16 +745,21 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
                 }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    float xv[8], o[8];
-                    load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(x + (c16 + q) * 128), 8, xv);
+                    const uint4 xv = *reinterpret_cast<const uint4 *>(x + (c16 + q) * 128);
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                    uint32_t o[4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        o[j] = fmaf(ea, __uint_as_float(e[8 * q + j]), __uint_as_float(u[8 * q + j]));
-                        if (p.D) o[j] = fmaf(D, xv[j], o[j]);
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = 8 * q + 2 * j;
+                        uint64_t f = fma2(ea2, pack2(e[at], e[at + 1]), pack2(u[at], u[at + 1]));
+                        if (p.D) f = fma2(D2, pack2(xw[j] << 16, xw[j] & 0xffff0000u), f);
+                        float lo, hi;
+                        unpack2(f, lo, hi);
+                        o[j] = pack_bf16(lo, hi);
                     }
                     // 16-byte pieces of a 128-byte row, moved by the row against conflicts
-                    store_vec<bf16, 8, true>(
-                        reinterpret_cast<bf16 *>(s.y + i * 128 + (((c16 + q) ^ (i & 7)) << 4)), 8, o);
+                    *reinterpret_cast<uint4 *>(s.y + i * 128 + (((c16 + q) ^ (i & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             warp_arrive(&s.x_free[it & 3]);

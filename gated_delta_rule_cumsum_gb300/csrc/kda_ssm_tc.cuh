@@ -86,6 +86,34 @@ struct RowDecays {
     float a[kTL], lo[kTL], d[kTL], fd[kTL], w[kTL], fi[kTL];
 };
 
+// Two fp32 values in a register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y) { return (uint64_t)y << 32 | x; }
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    return pack2(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &x, float &y) {
+    x = __uint_as_float((uint32_t)v);
+    y = __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    return fma2(b, 0xbf800000bf800000ull, a);  // a - b: exact products by -1, one rounding
+}
+
 // x = hi + lo in bf16 pairs: x0, x1 to about 2^-17 of each.
 __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
@@ -94,6 +122,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float x0, float x1) {
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x0, x1);
     lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+}
+__device__ __forceinline__ void split2p(uint64_t x, uint32_t &hi, uint32_t &lo) {
+    float x0, x1;
+    unpack2(x, x0, x1);
+    hi = pack_bf16(x0, x1);
+    unpack2(sub2(x, pack2(hi << 16, hi & 0xffff0000u)), x0, x1);
+    lo = pack_bf16(x0, x1);
 }
 // x = hi + mid + lo, to about 2^-25.
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
@@ -188,11 +223,24 @@ __device__ __forceinline__ void tmem_wait_ld() {
 // and marks the CTA dead; from then on no wait waits and no product is issued, but every
 // thread goes through the rest of its rounds, so that barriers match and the tensor memory
 // is freed.
+// The wait itself is the hardware's, for up to 20 us at a time: a warp that polled would take
+// issue slots from the warps it waits for.
+__device__ __forceinline__ bool suspended_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool wait_or_die(uint64_t *bar, uint32_t parity, volatile int *dead,
                                             int32_t *status) {
-    if (tc::mbar_try_wait(bar, parity)) return *dead == 0;
+    if (suspended_wait(bar, parity)) return *dead == 0;
     const uint64_t t0 = tc::globaltimer_ns();
-    while (!tc::mbar_try_wait(bar, parity)) {
+    while (!suspended_wait(bar, parity)) {
         if (*dead) return false;
         if (tc::globaltimer_ns() - t0 > kSsmWaitNs) {
             *dead = 1;

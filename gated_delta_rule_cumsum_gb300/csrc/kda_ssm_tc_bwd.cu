@@ -780,20 +780,24 @@ __global__ void __launch_bounds__(kTL) ssm_tc_step_grads_kernel(SsmArgs p) {
     }
 }
 
-// dB and dC rows of a chunk and group: the sum of the parts, in their order.
+// dB and dC rows of a chunk and group, 16 to a block: the sum of the parts, in their order.
+constexpr int kSumRows = 16;
 __global__ void __launch_bounds__(256) ssm_tc_group_sum_kernel(SsmArgs p) {
-    const int64_t sg = blockIdx.x;
+    const int64_t sg = blockIdx.x / (kTL / kSumRows);
+    const int row0 = (int)(blockIdx.x % (kTL / kSumRows)) * kSumRows;
     const int g = (int)(sg % p.G);
     TcChunk c;
     if (!tc_find_chunk(p, sg / p.G, c)) return;
     const int64_t tile = (int64_t)kTL * p.Ns;
     const float *b = p.dBh + sg * p.parts * tile, *cc = p.dCh + sg * p.parts * tile;
-    for (int e = threadIdx.x; e < c.nr * p.Ns / 4; e += 256) {
-        const int r = e * 4 / p.Ns, n = e * 4 % p.Ns;
+    const int per_row = p.Ns / 4;
+    for (int k = threadIdx.x; k < kSumRows * per_row; k += 256) {
+        const int r = row0 + k / per_row, n = k % per_row * 4, e = r * per_row + k % per_row;
+        if (r >= c.nr) break;
         float4 sb = make_float4(0.f, 0.f, 0.f, 0.f), sc = sb;
-        for (int k = 0; k < p.parts; ++k) {
-            const float4 x = *reinterpret_cast<const float4 *>(b + k * tile + e * 4);
-            const float4 y = *reinterpret_cast<const float4 *>(cc + k * tile + e * 4);
+        for (int q = 0; q < p.parts; ++q) {
+            const float4 x = *reinterpret_cast<const float4 *>(b + q * tile + e * 4);
+            const float4 y = *reinterpret_cast<const float4 *>(cc + q * tile + e * 4);
             sb.x += x.x; sb.y += x.y; sb.z += x.z; sb.w += x.w;
             sc.x += y.x; sc.y += y.y; sc.z += y.z; sc.w += y.w;
         }
@@ -801,9 +805,9 @@ __global__ void __launch_bounds__(256) ssm_tc_group_sum_kernel(SsmArgs p) {
         bf16 *dB = static_cast<bf16 *>(p.dB) + at, *dC = static_cast<bf16 *>(p.dC) + at;
         const float fb[4] = {sb.x, sb.y, sb.z, sb.w}, fc[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            dB[k] = __float2bfloat16_rn(fb[k]);
-            dC[k] = __float2bfloat16_rn(fc[k]);
+        for (int q = 0; q < 4; ++q) {
+            dB[q] = __float2bfloat16_rn(fb[q]);
+            dC[q] = __float2bfloat16_rn(fc[q]);
         }
     }
 }
@@ -872,7 +876,8 @@ cudaError_t launch_ssm_tc_bwd(const SsmArgs &a, cudaStream_t st) {
     cudaError_t e = bwd_setup();
     if (e != cudaSuccess) return e;
     const int64_t blocks = a.slots * a.G * a.parts, heads = a.slots * a.H;
-    if (blocks > INT32_MAX || heads > INT32_MAX) return cudaErrorInvalidValue;
+    if (blocks > INT32_MAX || heads > INT32_MAX || a.slots * a.G * (kTL / kSumRows) > INT32_MAX)
+        return cudaErrorInvalidValue;
     if (blocks == 0) return cudaSuccess;
     const bool al = aligned_to(a.x, 16) && aligned_to(a.Bm, 16) && aligned_to(a.Cm, 16) && aligned_to(a.dy, 16) &&
                     a.x_stride % 8 == 0 && a.b_stride % 8 == 0 && a.c_stride % 8 == 0;
@@ -889,7 +894,7 @@ cudaError_t launch_ssm_tc_bwd(const SsmArgs &a, cudaStream_t st) {
     prof_end(st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     prof_begin("ssm_tc_group_sum", st);
-    ssm_tc_group_sum_kernel<<<(unsigned)(a.slots * a.G), 256, 0, st>>>(a);
+    ssm_tc_group_sum_kernel<<<(unsigned)(a.slots * a.G * (kTL / kSumRows)), 256, 0, st>>>(a);
     prof_end(st);
     return cudaGetLastError();
 }
