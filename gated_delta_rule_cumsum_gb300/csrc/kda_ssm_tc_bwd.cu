@@ -291,7 +291,6 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
             const GradUnit u = w.at(p, it);
             auto &st = s.st[it & 1];
             const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
-            if (it + 1 < n) load(it + 1);  // into the stage of the unit before: its products are done
             wait_or_die(&s.full[it & 1], ph2, dead, p.status);
             const RowDecays &r = st.dec;
             const float ai = r.a[i], li = r.lo[i], ea = ex2_ftz(ai);
@@ -331,28 +330,47 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
                     uint32_t z[16], gm[16];
                     tmem_ld16_nowait(at, z);
                     tmem_ld16_nowait(tc::tmem_at(G, quad * 32, J * kSub), gm);
-                    const bool full = J < 2 * quad;
-                    const int e = J * kSub + kSub - 1;
-                    const float to_ref = ex2_ftz((ai - r.a[e]) + (li - r.lo[e]));
-                    tmem_wait_ld();
-                    float v[16], c[16];
+                    float c[16];  // Q, below the diagonal
+                    if (J < 2 * quad) {
+                        const int e = J * kSub + kSub - 1;
+                        const float to_ref = ex2_ftz((ai - r.a[e]) + (li - r.lo[e]));
+                        const uint64_t ref2 = pack2(to_ref, to_ref);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const uint64_t f = *reinterpret_cast<const uint64_t *>(&r.fd[J * kSub + 2 * q]);
+                            const uint64_t v = mul2(pack2(z[2 * q], z[2 * q + 1]), mul2(ref2, f));
+                            unpack2(mul2(v, pack2(gm[2 * q], gm[2 * q + 1])), c[2 * q], c[2 * q + 1]);
+                            split2p(v, o[q], o[8 + q]);
+                        }
+                    } else {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            float v[2];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int j = J * kSub + 2 * q + x;
+                                const float f = ex2_ftz((ai - r.a[j]) + (li - r.lo[j])) * r.d[j];
+                                // selects: above the diagonal the exponential may overflow
+                                v[x] = j <= i ? __uint_as_float(z[2 * q + x]) * f : 0.f;
+                                c[2 * q + x] = j < i ? v[x] * __uint_as_float(gm[2 * q + x]) : 0.f;
+                            }
+                            split2(v[0], v[1], o[q], o[8 + q]);
+                        }
+                    }
+                    // sums over the columns before t, of the rows i >= t: a column's place takes
+                    // the running sum of the row
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
-                        const int j = J * kSub + q;
-                        float f;
-                        if (full) {
-                            f = to_ref * r.fd[j];
-                        } else {
-                            f = ex2_ftz((ai - r.a[j]) + (li - r.lo[j])) * r.d[j];
-                            f = j <= i ? f : 0.f;
-                        }
-                        const float zf = j <= i ? __uint_as_float(z[q]) : 0.f;
-                        v[q] = zf * f;
-                        c[q] = j <= i ? before : 0.f;  // pairs (i, j' < j) with i >= j
-                        before += j < i ? v[q] * __uint_as_float(gm[q]) : 0.f;
+                        const float x = c[q];
+                        c[q] = before;
+                        before += x;
                     }
+                    if (J >= 2 * quad) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) split2(v[2 * q], v[2 * q + 1], o[q], o[8 + q]);
+                        for (int q = 0; q < 16; ++q) c[q] = J * kSub + q <= i ? c[q] : 0.f;
+                    }
                     const float sum = lane_sums(c);
                     if (lane < 16) s.rq[quad][J * kSub + lane] = sum;
                 }
@@ -362,6 +380,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
             tmem_wait_st();
             tc::tc_fence_before();
             warp_arrive(&s.w_ready);
+            if (it + 1 < n) load(it + 1);  // into the stage of the unit before: its products are done
             // u_i
             wait_or_die(&s.e_done, ph, dead, p.status);
             tc::tc_fence_after();
@@ -426,7 +445,7 @@ struct GradJSmem {
     uint8_t wx[2][kTL * kPT * 2];   // w x, hi and lo
     RowDecays dec[2];
     float qs[4][kTL], vs[4][kTL], dds[kGWarps];
-    uint64_t full[2], rows[2], z_done, wx_ready, xi_done, m_ready, done, cb;
+    uint64_t full[2], rows[2], z_done, wx_ready, xi_done, e_done, m_ready, done, cb;
     uint32_t slot_addr;
     int dead;
 };
@@ -448,6 +467,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
         }
         tc::mbar_init(&s.z_done, 1);
         tc::mbar_init(&s.xi_done, 1);
+        tc::mbar_init(&s.e_done, 1);
         tc::mbar_init(&s.done, 1);
         tc::mbar_init(&s.wx_ready, kGWarps);
         tc::mbar_init(&s.m_ready, kGWarps);
@@ -509,6 +529,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
                     mma_steps(dB, hi, 16, ek, 16, id, kPT / 16, it > 0);
                     mma_steps(dB, lo, 16, ek, 16, id, kPT / 16, 1);
                     mma_steps(dB, hi, 16, ek + elo, 16, id, kPT / 16, 1);
+                    tc::mma_commit(&s.e_done);
                 }
                 ok = ok && wait_or_die(&s.m_ready, ph, dead, p.status);
                 tc::tc_fence_after();
@@ -518,8 +539,8 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
                     mma_split(dB, W, cmn, 2 * NK, tc::idesc_bf16(128, NK, false, true), kTL / 16, 1);
                     tc::mma_commit(&s.done);
                 }
-                // E is free once this unit is multiplied
-                if (it + 1 < n && wait_or_die(&s.done, ph, dead, p.status)) fetch(it + 1);
+                // E is free: the products that read it come before those that wait for M
+                if (it + 1 < n && wait_or_die(&s.e_done, ph, dead, p.status)) fetch(it + 1);
             }
             if (*dead && fetched > 0) tc::mbar_wait(&s.full[(fetched - 1) & 1], ((fetched - 1) >> 1) & 1, 10000000ull);
         }
@@ -553,7 +574,6 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
         for (int it = 0; it < n; ++it) {
             const GradUnit u = w.at(p, it);
             const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
-            if (it + 1 < n) load(it + 1);
             wait_or_die(&s.full[it & 1], ph2, dead, p.status);
             const RowDecays &r = s.dec[it & 1];
             {   // w x in two parts: each thread's pieces, rows r0 and r0 + 64
@@ -586,31 +606,53 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
                 const int I = 2 * part + k;
                 const uint32_t mt = tc::tmem_at(M, quad * 32, I * kSub), wt = tc::tmem_at(W, quad * 32, I * kSub);
                 uint32_t om[16], ow[16];
+                uint64_t mo[8], zo[8];
                 if (I < 2 * quad) {
 #pragma unroll
                     for (int q = 0; q < 16; ++q) om[q] = ow[q] = 0u;
                 } else {
                     tmem_ld16_nowait(mt, om);
                     tmem_ld16_nowait(wt, ow);
-                    const bool full = I > 2 * quad + 1;
                     const float to_first = ex2_ftz((r.a[I * kSub] - aj) + (r.lo[I * kSub] - lj));
                     tmem_wait_ld();
-                    float m[16], z[16];
+                    if (I > 2 * quad + 1) {
+                        const uint64_t first2 = pack2(to_first, to_first), d2 = pack2(dj, dj);
+                        uint64_t sum2 = 0;
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const int i = I * kSub + q;
-                        const float f = full ? to_first * r.fi[i] : ex2_ftz((r.a[i] - aj) + (r.lo[i] - lj));
-                        const bool in = i >= j;
-                        const float zf = in ? __uint_as_float(ow[q]) * f : 0.f;
-                        const float gf = in ? __uint_as_float(om[q]) : 0.f;
-                        qsum = fmaf(zf, gf, qsum);
-                        m[q] = in ? gf * f * dj : 0.f;
-                        z[q] = zf * dj;
+                        for (int q = 0; q < 8; ++q) {
+                            const uint64_t f = mul2(first2, *reinterpret_cast<const uint64_t *>(&r.fi[I * kSub + 2 * q]));
+                            const uint64_t g = pack2(om[2 * q], om[2 * q + 1]);
+                            const uint64_t z = mul2(pack2(ow[2 * q], ow[2 * q + 1]), f);
+                            sum2 = fma2(z, g, sum2);
+                            mo[q] = mul2(g, mul2(f, d2));
+                            zo[q] = mul2(z, d2);
+                        }
+                        float x, y;
+                        unpack2(sum2, x, y);
+                        qsum += x + y;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            float m[2], z[2];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int i = I * kSub + 2 * q + x;
+                                const bool in = i >= j;  // selects: the exponential may overflow elsewhere
+                                const float f = ex2_ftz((r.a[i] - aj) + (r.lo[i] - lj));
+                                const float zf = in ? __uint_as_float(ow[2 * q + x]) * f : 0.f;
+                                const float gf = in ? __uint_as_float(om[2 * q + x]) : 0.f;
+                                qsum = fmaf(zf, gf, qsum);
+                                m[x] = in ? gf * f * dj : 0.f;
+                                z[x] = zf * dj;
+                            }
+                            mo[q] = pack2(m[0], m[1]);
+                            zo[q] = pack2(z[0], z[1]);
+                        }
                     }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
-                        split2(m[2 * q], m[2 * q + 1], om[q], om[8 + q]);
-                        split2(z[2 * q], z[2 * q + 1], ow[q], ow[8 + q]);
+                        split2p(mo[q], om[q], om[8 + q]);
+                        split2p(zo[q], ow[q], ow[8 + q]);
                     }
                 }
                 tmem_st16_nowait(mt, om);
@@ -619,6 +661,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             tmem_wait_st();
             tc::tc_fence_before();
             warp_arrive(&s.m_ready);
+            if (it + 1 < n) load(it + 1);
             s.qs[part][j] = qsum;
             // B E: its product with x, and its share of dx
             const int c16 = part * 2;
