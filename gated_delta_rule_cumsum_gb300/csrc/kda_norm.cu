@@ -3,7 +3,7 @@
 //
 //     h = x + res,   y = h w / sqrt(mean(h^2) + eps)
 //     8 bits: scale = max |y| / top over a row (or over 128 columns of it; 1 where every
-//     y is 0), q = round(y / scale), top = 448 (e4m3) or 127 (int8)
+//     y is 0, NaN where one is), q = round(y / scale), top = 448 (e4m3) or 127 (int8)
 //
 // A row stays in its threads' registers between the sums and the output, so every input
 // is read once and every output written once: bandwidth-bound (2 flops a byte).  The sum
@@ -37,15 +37,22 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float *red) {
         v[i] = s;
     }
 }
+// The larger, or NaN if either is NaN: a NaN in a row has to show in its scale, since int8
+// has no code for it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float row_max(float v, int tpr, float *red) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     if (tpr == 32) return v;
     const int warps = tpr >> 5, warp = threadIdx.x >> 5, first = (threadIdx.x / tpr) * warps;
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     __syncthreads();
-    for (int k = 0; k < warps; ++k) v = fmaxf(v, red[first + k]);
+    for (int k = 0; k < warps; ++k) v = max_nan(v, red[first + k]);
     return v;
 }
 
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 v[i][j] = v[i][j] * rstd * w[i][j];
-                if (Q) amax = fmaxf(amax, fabsf(v[i][j]));
+                if (Q) amax = max_nan(amax, fabsf(v[i][j]));
             }
             if constexpr (!Q)
                 if (live && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.y) + row * p.cols + c, n, v[i]);
@@ -191,12 +198,13 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd
                 if (p.group) {
                     m = 0.f;
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) m = fmaxf(m, fabsf(v[i][j]));
+                    for (int j = 0; j < VEC; ++j) m = max_nan(m, fabsf(v[i][j]));
 #pragma unroll
                     for (int o = 64 / VEC; o > 0; o >>= 1)
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 }
-                const float scale = m > 0.f ? m / top : 1.f;
+                // at least the smallest normal number, so that 1 / scale is finite
+                const float scale = m == 0.f ? 1.f : max_nan(m / top, 1.17549435e-38f);
                 const float inv = 1.f / scale;
                 if (live && n > 0) {
                     if (p.group ? c % 128 == 0 : c == 0)

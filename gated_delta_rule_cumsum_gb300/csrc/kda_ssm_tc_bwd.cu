@@ -96,8 +96,6 @@ __device__ __forceinline__ void load_wide(uint8_t *tile, const bf16 *src, int64_
         }
     }
 }
-__device__ __forceinline__ void commit_loads() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void wait_all_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 // The sums over a warp's 32 lanes of each of 16 values: lane l ends with that of value l % 16.
 __device__ __forceinline__ float lane_sums(float (&v)[16]) {

@@ -463,9 +463,12 @@ size_t kda_chunk_bwd_workspace_size(const kda_shape *shape);
  * State caches.  The step entry points update one row of a cache per batch row, in
  * place: state_indices[n] is row n's slot (NULL: slot n).  A negative entry marks an
  * unused batch row: no state is touched and its output is zero.  An entry past the last
- * slot sets KDA_DEVICE_BAD_INDEX, and its row is skipped like an unused one.  Entries must be distinct: two
- * rows of one slot race.
- * Non-finite inputs make the values that depend on them non-finite and no others.
+ * slot sets KDA_DEVICE_BAD_INDEX, and its row is skipped like an unused one.  Entries must
+ * be distinct: two rows of one slot race.
+ * Non-finite inputs make the outputs that depend on them non-finite, and of the forward
+ * functions, the steps, the convolution's and the norm's gradients no others.  In the scan's
+ * gradients they may reach further: to all rows of their chunk (up to 128 rows of the same
+ * sequence) in the same head, and in dB and dC in the same group.
  */
 
 /* flags of kda_conv_shape */
@@ -593,7 +596,8 @@ typedef struct {
  * kda_add_rmsnorm_fwd -- h = x + residual (residual NULL: h = x),
  *     y = h w / sqrt(mean(h^2) + eps),
  * and for the 8-bit outputs, per row or group of columns, scale = max|y| / top (1 where
- * that is 0 or not a number) and y rounded to q = y / scale, ties to even.
+ * every y is 0, at least the smallest normal number elsewhere, and not a number where a y
+ * is not) and y rounded to q = y / scale, ties to even.
  *   x, residual, h  [rows, cols] (h may be NULL: not stored); the norm takes the unrounded sum
  *   w               [cols] fp32
  *   y               [rows, cols]: the shape's type, or one byte per element

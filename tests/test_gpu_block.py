@@ -414,9 +414,24 @@ def test_norm_non_finite_rows(kda_lib):
     x[1, 5], x[2, 7] = float("nan"), float("inf")
     y = kda_lib.add_rms_norm(x, w)[0]
     assert torch.equal(y[[0, 3]], clean[[0, 3]]) and torch.isnan(y[1]).all()
-    for kind in ("e4m3", "int8"):
+    for kind in ("e4m3", "int8"):  # int8 has no code for NaN: it shows in the scale
         _, scale, _ = kda_lib.add_rms_norm_quant(x, w, out_dtype=kind)
-        assert scale[1] == 1 and torch.isfinite(scale).all()
+        assert torch.isnan(scale[[1, 2]]).all() and torch.isfinite(scale[[0, 3]]).all()
+        # of the row with the infinity, only its own group (0 inf; the other columns are 0)
+        _, scale, _ = kda_lib.add_rms_norm_quant(x, w, out_dtype=kind, group=128)
+        assert torch.isnan(scale[1]).all() and torch.isnan(scale[2, 0]) and (scale[2, 1:] == 1).all()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_norm_quantised_tiny_values(kda_lib, kind):
+    """Largest values whose quotient by the top leaves the normal range: the scale stays the
+    smallest normal number, and q * scale within half a step of it."""
+    x = torch.ones(2, 64, device="cuda")
+    w = torch.full((64,), 2.0 ** -125, device="cuda")
+    w[1::2] = -(2.0 ** -126)
+    q, scale, _ = kda_lib.add_rms_norm_quant(x, w, eps=0.0, out_dtype=kind)
+    assert (scale == 2.0 ** -126).all()
+    assert torch.equal(q.float(), (w * 2.0 ** 126).expand(2, 64))
 
 
 def test_norm_gradient_against_differences(kda_lib):
