@@ -123,6 +123,34 @@ struct SsmStepArgs {
 cudaError_t launch_ssm_step(const SsmStepArgs &a, kda_dtype dt, cudaStream_t st);
 
 // ---------------------------------------------------------------------- helpers
+// Two fp32 values in a register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y) { return (uint64_t)y << 32 | x; }
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    return pack2(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &x, float &y) {
+    x = __uint_as_float((uint32_t)v);
+    y = __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    return fma2(b, 0xbf800000bf800000ull, a);  // a - b: exact products by -1, one rounding
+}
+
 // VEC consecutive elements as fp32: one vector load when the address is aligned for it
 // (ALIGNED), else scalar loads of the first `n`, zeros after.
 template <typename T, int VEC, bool ALIGNED>
