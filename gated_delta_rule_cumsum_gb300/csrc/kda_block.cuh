@@ -54,7 +54,7 @@ struct NormArgs {
     void *dx;
     float *dw, *part;
 };
-int64_t norm_bwd_parts(int64_t rows, int cols);
+int64_t norm_bwd_parts(int64_t rows, int cols, kda_dtype dt);
 cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st);
 

@@ -385,7 +385,7 @@ kda_status kda_add_rmsnorm_fwd(const void *x, const void *residual, const float 
 }
 
 size_t kda_add_rmsnorm_bwd_workspace_size(const kda_norm_shape *s) {
-    return norm_ok(s) ? (size_t)kda::norm_bwd_parts(s->rows, s->cols) * s->cols * 4 : 0;
+    return norm_ok(s) ? (size_t)kda::norm_bwd_parts(s->rows, s->cols, s->dtype) * s->cols * 4 : 0;
 }
 
 kda_status kda_add_rmsnorm_bwd(const void *dy, const void *h, const float *w, const void *dh,

@@ -10,13 +10,16 @@
 // h is kept in fp32 for the norm; the stored h is rounded once, beside it.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "kda_block.cuh"
 
 namespace kda {
 namespace {
 
 // Threads that share a row: `tpr` (a multiple of 32); blockDim.x / tpr rows per block.
-// red holds one float per warp and value.
+// red holds one float per warp and value; a caller takes two in turn, so that a warp which
+// is one sum ahead writes the other one.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float *red) {
 #pragma unroll
@@ -25,7 +28,6 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int tpr, float *red) {
         for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     if (tpr == 32) return;
     const int warps = tpr >> 5, warp = threadIdx.x >> 5, first = (threadIdx.x / tpr) * warps;
-    __syncthreads();  // the previous use of red is over
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
         for (int i = 0; i < N; ++i) red[i * 32 + warp] = v[i];
@@ -49,7 +51,6 @@ __device__ __forceinline__ float row_max(float v, int tpr, float *red) {
     for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     if (tpr == 32) return v;
     const int warps = tpr >> 5, warp = threadIdx.x >> 5, first = (threadIdx.x / tpr) * warps;
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) red[warp] = v;
     __syncthreads();
     for (int k = 0; k < warps; ++k) v = max_nan(v, red[first + k]);
@@ -108,10 +109,17 @@ struct alignas(VEC * sizeof(T)) Vec {
         for (int j = 0; j < VEC; ++j) v[j] = from_f32<T>(0.f);
     }
     __device__ __forceinline__ void widen(float (&f)[VEC]) const { load_vec<T, VEC, true>(v, VEC, f); }
+    // in pairs, for the packed operations
+    __device__ __forceinline__ void widen(uint64_t (&f)[VEC / 2]) const {
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(v);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j)
+            f[j] = sizeof(T) == 4 ? pack2(u[2 * j], u[2 * j + 1]) : pack2(u[j] << 16, u[j] & 0xffff0000u);
+    }
 };
-// Blocks that an SM holds: of 256 threads four with one or two vectors per thread (64
-// registers), three in the backward and two with four, which need more of them.
-constexpr int blocks_per_sm(int maxt, int nv, bool bwd) { return maxt > 256 ? 1 : nv == 4 ? 2 : bwd ? 3 : 4; }
+// Blocks of MAXT threads that an SM holds in the forward: of 256 threads four with one or two
+// vectors per thread (64 registers), two with four, which need more of them.
+constexpr int blocks_per_sm(int maxt, int nv) { return maxt > 256 ? 1 : nv == 4 ? 2 : 4; }
 
 // NV vectors of VEC columns per thread: thread i of a row holds vectors i, i + tpr, ...
 // Eight (bf16) or four (fp32) adjacent columns per thread make a 128-column scale group
@@ -119,8 +127,8 @@ constexpr int blocks_per_sm(int maxt, int nv, bool bwd) { return maxt > 256 ? 1 
 // the weights stay in registers, and a row's loads are issued while the row before it is
 // summed and stored.
 template <typename T, int VEC, int NV, bool AL, bool Q, int MAXT>
-__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd_kernel(NormArgs p, int tpr) {
-    __shared__ float red[32];
+__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV)) norm_fwd_kernel(NormArgs p, int tpr) {
+    __shared__ float red[2][2][32];  // [sum, largest], in turn
     const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
     const int64_t first = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr, step = (int64_t)gridDim.x * rpb;
     // every thread makes the same number of rounds: the sums have block-wide barriers
@@ -173,7 +181,7 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd
                 if (live && n > 0) store_vec<T, VEC, AL>(h + c, n, v[i]);
             }
         }
-        row_sum<1>(ss, tpr, red);
+        row_sum<1>(ss, tpr, red[0][k & 1]);
         const float rstd = 1.f / sqrtf(ss[0] / (float)p.cols + p.eps);
         float amax = 0.f;
 #pragma unroll
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd
         if constexpr (Q) {
             const float top = p.out == KDA_NORM_E4M3 ? 448.f : 127.f;
             uint8_t *q = static_cast<uint8_t *>(p.y) + row * p.cols;
-            if (p.group == 0) amax = row_max(amax, tpr, red);
+            if (p.group == 0) amax = row_max(amax, tpr, red[1][k & 1]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
@@ -223,67 +231,80 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, false)) norm_fwd
 // Both row sums (h^2 and g h) come from one exchange.  The grid walks over the rows as the
 // forward's does; a thread keeps its columns' share of dw in registers and leaves it in p.part,
 // and a second kernel adds the shares in a fixed order.
-template <typename T, int VEC, int NV, bool AL, int MAXT>
-__global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, true)) norm_bwd_kernel(NormArgs p, int tpr) {
-    __shared__ float red[64];
+// Two vectors per thread (of eight columns in bf16, four in fp32) rather than as many threads:
+// what a row costs beside its columns (sums over threads, addresses, a barrier) is shared.
+template <typename T, int VEC, int NV, bool AL, int MAXT, int BLOCKS>
+__global__ void __launch_bounds__(MAXT, BLOCKS) norm_bwd_kernel(NormArgs p, int tpr) {
+    __shared__ float red[2][64];
+    constexpr int VP = VEC / 2;
     const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
-    float dw[NV][VEC] = {}, w[NV][VEC];
+    uint64_t dw[NV][VP] = {}, w[NV][VP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) w[i][j] = j < n ? p.w[c + j] : 0.f;
+        for (int j = 0; j < VP; ++j)
+            w[i][j] = pack2(2 * j < n ? p.w[c + 2 * j] : 0.f, 2 * j + 1 < n ? p.w[c + 2 * j + 1] : 0.f);
     }
     const int64_t first = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr, step = (int64_t)gridDim.x * rpb;
-    const int64_t rounds = (p.rows + step - 1) / step;
+    const int64_t rounds = (p.rows + step - 1) / step, apart = step * p.cols;
     Vec<T, VEC, AL> hn[NV], gn[NV], rn[NV];
-    auto fetch = [&](int64_t row) {
-        const int64_t at = row * p.cols;
+    int64_t at = first * p.cols + tid * VEC;  // of the row in hand; the next one's are on their way
+    auto fetch = [&](int64_t row, int64_t next) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            const int n = min(VEC, p.cols - (tid + i * tpr) * VEC);
             hn[i].zero();
             gn[i].zero();
             rn[i].zero();
             if (row < p.rows && n > 0) {
-                hn[i].load(static_cast<const T *>(p.h) + at + c, n);
-                gn[i].load(static_cast<const T *>(p.dy) + at + c, n);
-                if (p.dres) rn[i].load(static_cast<const T *>(p.dres) + at + c, n);
+                hn[i].load(static_cast<const T *>(p.h) + next + i * tpr * VEC, n);
+                gn[i].load(static_cast<const T *>(p.dy) + next + i * tpr * VEC, n);
+                if (p.dres) rn[i].load(static_cast<const T *>(p.dres) + next + i * tpr * VEC, n);
             }
         }
     };
-    fetch(first);
-    for (int64_t k = 0; k < rounds; ++k) {
-        const int64_t row = first + k * step, at = row * p.cols;
-        const bool live = row < p.rows;
-        float h[NV][VEC], g[NV][VEC], r[NV][VEC];
-        float s[2] = {0.f, 0.f};
+    fetch(first, at);
+    for (int64_t k = 0; k < rounds; ++k, at += apart) {
+        const int64_t row = first + k * step;
+        uint64_t h[NV][VP], g[NV][VP], s2[2] = {0, 0};
+        Vec<T, VEC, AL> r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             hn[i].widen(h[i]);
             gn[i].widen(g[i]);
-            rn[i].widen(r[i]);
+            r[i] = rn[i];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                s[0] = fmaf(h[i][j], h[i][j], s[0]);
-                s[1] = fmaf(g[i][j] * w[i][j], h[i][j], s[1]);
+            for (int j = 0; j < VP; ++j) {
+                s2[0] = fma2(h[i][j], h[i][j], s2[0]);
+                s2[1] = fma2(mul2(g[i][j], w[i][j]), h[i][j], s2[1]);
             }
         }
-        if (k + 1 < rounds) fetch(row + step);
-        row_sum<2>(s, tpr, red);
+        if (k + 1 < rounds) fetch(row + step, at + apart);
+        float s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float x, y;
+            unpack2(s2[i], x, y);
+            s[i] = x + y;
+        }
+        row_sum<2>(s, tpr, red[k & 1]);
         const float rstd = 1.f / sqrtf(s[0] / (float)p.cols + p.eps);
-        const float m = s[1] / (float)p.cols * rstd;  // mean(g xhat)
+        const float m = -s[1] / (float)p.cols * rstd;  // - mean(g xhat)
+        const uint64_t rstd2 = pack2(rstd, rstd), m2 = pack2(m, m);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
+            const int n = min(VEC, p.cols - (tid + i * tpr) * VEC);
+            uint64_t res[VP];
+            r[i].widen(res);
             float o[VEC];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float xh = h[i][j] * rstd;
-                dw[i][j] = fmaf(g[i][j], xh, dw[i][j]);
-                o[j] = fmaf(rstd, fmaf(g[i][j], w[i][j], -xh * m), r[i][j]);
+            for (int j = 0; j < VP; ++j) {
+                const uint64_t xh = mul2(h[i][j], rstd2);
+                dw[i][j] = fma2(g[i][j], xh, dw[i][j]);
+                unpack2(fma2(rstd2, fma2(xh, m2, mul2(g[i][j], w[i][j])), res[j]), o[2 * j], o[2 * j + 1]);
             }
-            if (live && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.dx) + at + c, n, o);
+            if (row < p.rows && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.dx) + at + i * tpr * VEC, n, o);
         }
     }
     float *part = p.part + first * p.cols;
@@ -291,8 +312,12 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV, true)) norm_bwd_
     for (int i = 0; i < NV; ++i) {
         const int c = (tid + i * tpr) * VEC;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            if (c + j < p.cols) part[c + j] = dw[i][j];
+        for (int j = 0; j < VP; ++j) {
+            float x, y;
+            unpack2(dw[i][j], x, y);
+            if (c + 2 * j < p.cols) part[c + 2 * j] = x;
+            if (c + 2 * j + 1 < p.cols) part[c + 2 * j + 1] = y;
+        }
     }
 }
 
@@ -315,25 +340,26 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, i
     }
 }
 
-// Threads per row, vectors per thread and rows per block of a row of `vecs` vectors: the
-// fewest vectors per thread (1, 2 or 4) that keep a row within 256 threads, and four with
-// up to 1024 threads for the longest rows (16384 columns); short rows share a block of 128
-// threads.
+// Threads per row, vectors per thread and rows per block of a row of `vecs` vectors; short
+// rows share a block of 128 threads.
 struct RowPlan {
     int tpr, nv, rpb;
 };
-RowPlan row_plan(int vecs) {
+RowPlan plan_of(int vecs, int nv) {
     RowPlan r{};
-    for (int nv : {1, 2, 4}) {
-        const int t = ((vecs + nv - 1) / nv + 31) / 32 * 32;
-        if (t <= 256 || (nv == 4 && t <= 1024)) {
-            r.tpr = t;
-            r.nv = nv;
-            r.rpb = t < 128 ? 128 / t : 1;
-            return r;
-        }
-    }
+    r.nv = nv;
+    r.tpr = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+    r.rpb = r.tpr < 128 ? 128 / r.tpr : 1;
     return r;
+}
+// Forward: the fewest vectors per thread (1, 2 or 4) that keep a row within 256 threads, and
+// four with up to 1024 threads for the longest rows (16384 columns).
+RowPlan fwd_plan(int vecs) { return plan_of(vecs, vecs <= 256 ? 1 : vecs <= 512 ? 2 : 4); }
+// Backward: two vectors per thread from 64 vectors on, and four of fp32 where two would take
+// more than 512 threads.
+RowPlan bwd_plan(int cols, bool bf) {
+    const int vecs = bf ? (cols + 7) / 8 : (cols + 3) / 4;
+    return plan_of(vecs, vecs <= 64 ? 1 : bf || vecs <= 1024 ? 2 : 4);
 }
 
 bool norm_aligned(const NormArgs &a, size_t e, const void *const *ptrs, int count) {
@@ -358,18 +384,20 @@ void by_plan(const RowPlan &r, F &&f) {
 
 // Blocks of either direction: what the GPU's 152 SMs hold at once, at most one per row (the
 // backward leaves one row of partial sums per row that a block works on at a time).
-int64_t row_blocks(int64_t rows, const RowPlan &r, bool bwd) {
-    const int threads = r.tpr * r.rpb;
-    const int per_sm = threads > 256 ? 1 : blocks_per_sm(256, r.nv, bwd) * 256 / threads;
-    const int64_t want = 152 * (int64_t)per_sm, most = (rows + r.rpb - 1) / r.rpb;
-    return want < most ? want : most;
+int64_t row_blocks(int64_t rows, const RowPlan &r, int threads_per_sm) {
+    const int64_t want = 152 * (int64_t)std::max(threads_per_sm / (r.tpr * r.rpb), 1);
+    return std::min(want, (rows + r.rpb - 1) / r.rpb);
 }
+int64_t fwd_blocks(int64_t rows, const RowPlan &r) {
+    return row_blocks(rows, r, r.tpr > 256 ? 1024 : 256 * blocks_per_sm(256, r.nv));
+}
+int64_t bwd_blocks(int64_t rows, const RowPlan &r) { return row_blocks(rows, r, r.nv == 1 ? 768 : 512); }
 
 }  // namespace
 
-int64_t norm_bwd_parts(int64_t rows, int cols) {
-    const RowPlan r = row_plan((cols + 3) / 4);
-    return r.tpr == 0 ? 0 : row_blocks(rows, r, true) * r.rpb;
+int64_t norm_bwd_parts(int64_t rows, int cols, kda_dtype dt) {
+    const RowPlan r = bwd_plan(cols, dt == KDA_DTYPE_BF16);
+    return bwd_blocks(rows, r) * r.rpb;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
@@ -378,9 +406,9 @@ cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
     const bool bf = dt == KDA_DTYPE_BF16, q = a.out != KDA_NORM_SAME;
     const bool al = norm_aligned(a, bf ? 2 : 4, ptrs, 4);
     const int vec = bf ? 8 : 4;
-    const RowPlan r = row_plan((a.cols + vec - 1) / vec);
-    if (r.tpr == 0) return cudaErrorInvalidValue;
-    const int64_t blocks = row_blocks(a.rows, r, false);
+    const RowPlan r = fwd_plan((a.cols + vec - 1) / vec);
+    if (r.tpr > 1024) return cudaErrorInvalidValue;
+    const int64_t blocks = fwd_blocks(a.rows, r);
     prof_begin("norm_fwd", st);
     by_plan(r, [&](auto NV, auto MAXT) {
         const unsigned g = (unsigned)blocks, t = (unsigned)(r.tpr * r.rpb);
@@ -409,25 +437,35 @@ cudaError_t launch_norm_fwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
 cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
     const bool bf = dt == KDA_DTYPE_BF16;
     const void *ptrs[] = {a.h, a.dy, a.dres, a.dx};
-    // four columns per thread in both types: dw and the three inputs of eight would not
-    // leave room in registers for a second block
-    bool al = aligned_to(a.w, 4) && ((size_t)a.cols * (bf ? 2 : 4)) % (bf ? 8 : 16) == 0;
-    for (const void *q : ptrs) al = al && aligned_to(q, bf ? 8 : 16);
-    const RowPlan r = row_plan((a.cols + 3) / 4);
-    if (r.tpr == 0) return cudaErrorInvalidValue;
-    const int64_t blocks = row_blocks(a.rows, r, true);
+    const bool al = norm_aligned(a, bf ? 2 : 4, ptrs, 4);
+    const RowPlan r = bwd_plan(a.cols, bf);
+    if (r.tpr > 1024) return cudaErrorInvalidValue;
+    const int64_t blocks = bwd_blocks(a.rows, r);
     if (blocks > 0) {
+        using std::integral_constant;
         prof_begin("norm_bwd", st);
-        by_plan(r, [&](auto NV, auto MAXT) {
+        auto go = [&](auto NV, auto MAXT, auto BLOCKS) {
             const unsigned g = (unsigned)blocks, t = (unsigned)(r.tpr * r.rpb);
-            if (bf) {
-                if (al) norm_bwd_kernel<__nv_bfloat16, 4, NV(), true, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
-                else norm_bwd_kernel<__nv_bfloat16, 4, NV(), false, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
-            } else {
-                if (al) norm_bwd_kernel<float, 4, NV(), true, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
-                else norm_bwd_kernel<float, 4, NV(), false, MAXT()><<<g, t, 0, st>>>(a, r.tpr);
+            constexpr int nv = NV(), maxt = MAXT(), per_sm = BLOCKS();
+            if constexpr (nv <= 2) {
+                if (bf && al) norm_bwd_kernel<__nv_bfloat16, 8, nv, true, maxt, per_sm><<<g, t, 0, st>>>(a, r.tpr);
+                if (bf && !al) norm_bwd_kernel<__nv_bfloat16, 8, nv, false, maxt, per_sm><<<g, t, 0, st>>>(a, r.tpr);
             }
-        });
+            if constexpr (nv == 4 || maxt <= 512) {
+                if (!bf && al) norm_bwd_kernel<float, 4, nv, true, maxt, per_sm><<<g, t, 0, st>>>(a, r.tpr);
+                if (!bf && !al) norm_bwd_kernel<float, 4, nv, false, maxt, per_sm><<<g, t, 0, st>>>(a, r.tpr);
+            }
+        };
+        using One = integral_constant<int, 1>;
+        using Two = integral_constant<int, 2>;
+        using Four = integral_constant<int, 4>;
+        using Short = integral_constant<int, 256>;
+        using Long = integral_constant<int, 512>;
+        using Longest = integral_constant<int, 1024>;
+        if (r.nv == 1) go(One(), Short(), integral_constant<int, 3>());
+        else if (r.nv == 2 && r.tpr <= 256) go(Two(), Short(), Two());
+        else if (r.nv == 2) r.tpr <= 512 ? go(Two(), Long(), One()) : go(Two(), Longest(), One());
+        else r.tpr <= 512 ? go(Four(), Long(), One()) : go(Four(), Longest(), One());
         prof_end(st);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
