@@ -57,9 +57,30 @@ __device__ __forceinline__ float row_max(float v, int tpr, float *red) {
     return v;
 }
 
-// VEC 8-bit values, vector-stored when ALIGNED.
+// The j-th column of a row's vector v.  Vector loads want a thread's columns adjacent; where
+// rows are not aligned for those, a warp's 32 VEC columns are dealt to its lanes in turn, so
+// that each scalar access of the warp is still contiguous (8192 x 4095 bf16: 98 us forward
+// against 175 with adjacent columns; the backward, whose time is in its sums, keeps them
+// adjacent: 147 us against 138, but 166 against 197 at 16384 x 2049).  Either way a group of 128 columns lies in one warp.
 template <int VEC, bool AL>
-__device__ __forceinline__ void store_q(uint8_t *p, int n, const float (&v)[VEC], int out) {
+__device__ __forceinline__ int col_of(int v, int j) {
+    return AL ? v * VEC + j : (v & ~31) * VEC + (v & 31) + 32 * j;
+}
+// The columns of vector v, converted, to a row of `cols` columns.
+template <typename T, int VEC, bool AL>
+__device__ __forceinline__ void store_cols(T *row, int v, int cols, const float (&f)[VEC]) {
+    if constexpr (AL) {
+        if (v * VEC < cols) store_vec<T, VEC, true>(row + v * VEC, VEC, f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (col_of<VEC, AL>(v, j) < cols) row[col_of<VEC, AL>(v, j)] = from_f32<T>(f[j]);
+    }
+}
+
+// The same to 8 bits.
+template <int VEC, bool AL>
+__device__ __forceinline__ void store_q(uint8_t *row, int c, int cols, const float (&v)[VEC], int out) {
     union {
         uint8_t b[VEC];
         uint32_t w[VEC / 4];
@@ -77,14 +98,14 @@ __device__ __forceinline__ void store_q(uint8_t *p, int n, const float (&v)[VEC]
         for (int i = 0; i < VEC; ++i)
             u.b[i] = (uint8_t)(int8_t)__float2int_rn(fminf(fmaxf(v[i], -127.f), 127.f));
     }
-    if constexpr (AL && VEC == 8) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(u.w[0], u.w[1]);
-    } else if constexpr (AL) {
-        *reinterpret_cast<uint32_t *>(p) = u.w[0];
+    if constexpr (AL) {
+        if (c * VEC >= cols) return;
+        if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(row + c * VEC) = make_uint2(u.w[0], u.w[1]);
+        else *reinterpret_cast<uint32_t *>(row + c * VEC) = u.w[0];
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-            if (i < n) p[i] = u.b[i];
+            if (col_of<VEC, AL>(c, i) < cols) row[col_of<VEC, AL>(c, i)] = u.b[i];
     }
 }
 
@@ -92,16 +113,24 @@ __device__ __forceinline__ void store_q(uint8_t *p, int n, const float (&v)[VEC]
 template <typename T, int VEC, bool AL>
 struct alignas(VEC * sizeof(T)) Vec {
     T v[VEC];
+    // VEC adjacent columns, the first n of them where the row is not aligned
     __device__ __forceinline__ void load(const T *p, int n) {
+        static_assert(VEC * sizeof(T) == 16, "vectors of 16 bytes");
         if constexpr (AL) {
-            constexpr int B = VEC * (int)sizeof(T);
-            if constexpr (B == 16)
-                *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
-            else
-                *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
+            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p);
         } else {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) v[j] = j < n ? p[j] : from_f32<T>(0.f);
+        }
+    }
+    // the columns of vector c of a row of `cols` columns; those past them stay
+    __device__ __forceinline__ void load_cols(const T *row, int c, int cols) {
+        if constexpr (AL) {
+            if (c * VEC < cols) load(row + c * VEC, VEC);
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if (col_of<VEC, AL>(c, j) < cols) v[j] = row[col_of<VEC, AL>(c, j)];
         }
     }
     __device__ __forceinline__ void zero() {
@@ -138,7 +167,7 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV)) norm_fwd_kernel
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            const int c = (tid + i * tpr) * VEC + j;
+            const int c = col_of<VEC, AL>(tid + i * tpr, j);
             w[i][j] = c < p.cols ? p.w[c] : 0.f;
         }
     Vec<T, VEC, AL> xn[NV], rn[NV];
@@ -146,12 +175,11 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV)) norm_fwd_kernel
         const T *x = static_cast<const T *>(p.x) + row * p.cols, *r = static_cast<const T *>(p.res) + row * p.cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
             xn[i].zero();  // rows and columns past the last add nothing
             rn[i].zero();
-            if (row < p.rows && n > 0) {
-                xn[i].load(x + c, n);
-                if (p.res) rn[i].load(r + c, n);
+            if (row < p.rows) {
+                xn[i].load_cols(x, tid + i * tpr, p.cols);
+                if (p.res) rn[i].load_cols(r, tid + i * tpr, p.cols);
             }
         }
     };
@@ -176,24 +204,21 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV)) norm_fwd_kernel
         if (p.h) {
             T *h = static_cast<T *>(p.h) + row * p.cols;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-                if (live && n > 0) store_vec<T, VEC, AL>(h + c, n, v[i]);
-            }
+            for (int i = 0; i < NV; ++i)
+                if (live) store_cols<T, VEC, AL>(h, tid + i * tpr, p.cols, v[i]);
         }
         row_sum<1>(ss, tpr, red[0][k & 1]);
         const float rstd = 1.f / sqrtf(ss[0] / (float)p.cols + p.eps);
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 v[i][j] = v[i][j] * rstd * w[i][j];
                 if (Q) amax = max_nan(amax, fabsf(v[i][j]));
             }
             if constexpr (!Q)
-                if (live && n > 0) store_vec<T, VEC, AL>(static_cast<T *>(p.y) + row * p.cols + c, n, v[i]);
+                if (live) store_cols<T, VEC, AL>(static_cast<T *>(p.y) + row * p.cols, tid + i * tpr, p.cols, v[i]);
         }
         if constexpr (Q) {
             const float top = p.out == KDA_NORM_E4M3 ? 448.f : 127.f;
@@ -201,26 +226,30 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV)) norm_fwd_kernel
             if (p.group == 0) amax = row_max(amax, tpr, red[1][k & 1]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (tid + i * tpr) * VEC, n = min(VEC, p.cols - c);
-                float m = amax;
-                if (p.group) {
-                    m = 0.f;
+                // scales of the vector's columns: one, or (dealt to the lanes) one per four
+                constexpr int S = AL ? 1 : VEC / 4;
+                const int c = tid + i * tpr;
+                float m[S], inv[S];
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) m = max_nan(m, fabsf(v[i][j]));
+                for (int s = 0; s < S; ++s) {
+                    m[s] = p.group ? 0.f : amax;
+                    if (p.group) {
 #pragma unroll
-                    for (int o = 64 / VEC; o > 0; o >>= 1)
-                        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        for (int j = 0; j < VEC / S; ++j) m[s] = max_nan(m[s], fabsf(v[i][VEC / S * s + j]));
+#pragma unroll
+                        for (int o = AL ? 64 / VEC : 16; o > 0; o >>= 1)
+                            m[s] = max_nan(m[s], __shfl_xor_sync(0xffffffffu, m[s], o));
+                    }
+                    // at least the smallest normal number, so that 1 / scale is finite
+                    const float scale = m[s] == 0.f ? 1.f : max_nan(m[s] / top, 1.17549435e-38f);
+                    inv[s] = 1.f / scale;
+                    const int first = col_of<VEC, AL>(c, VEC / S * s);
+                    if (live && first < p.cols && (p.group ? first % 128 == 0 : first == 0))
+                        p.scale[row * groups + (p.group ? first / 128 : 0)] = scale;
                 }
-                // at least the smallest normal number, so that 1 / scale is finite
-                const float scale = m == 0.f ? 1.f : max_nan(m / top, 1.17549435e-38f);
-                const float inv = 1.f / scale;
-                if (live && n > 0) {
-                    if (p.group ? c % 128 == 0 : c == 0)
-                        p.scale[row * groups + (p.group ? c / 128 : 0)] = scale;
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) v[i][j] *= inv;
-                    store_q<VEC, AL>(q + c, n, v[i], p.out);
-                }
+                for (int j = 0; j < VEC; ++j) v[i][j] *= inv[j * S / VEC];
+                if (live) store_q<VEC, AL>(q, c, p.cols, v[i], p.out);
             }
         }
     }
@@ -352,11 +381,13 @@ RowPlan plan_of(int vecs, int nv) {
     r.rpb = r.tpr < 128 ? 128 / r.tpr : 1;
     return r;
 }
-// Forward: the fewest vectors per thread (1, 2 or 4) that keep a row within 256 threads, and
-// four with up to 1024 threads for the longest rows (16384 columns).
+// Forward: the fewest vectors per thread (1, 2 or 4) that keep a row within 256 threads
+// (16384 x 2048 bf16: 43.5 us, 47.9 with two), and four with up to 1024 threads for the
+// longest rows (16384 columns).
 RowPlan fwd_plan(int vecs) { return plan_of(vecs, vecs <= 256 ? 1 : vecs <= 512 ? 2 : 4); }
-// Backward: two vectors per thread from 64 vectors on, and four of fp32 where two would take
-// more than 512 threads.
+// Backward: two vectors per thread from 64 vectors on (8192 x 2048 bf16: 27 us against 32 with
+// one; 16384 x 1024: 29.4 against 30.6), and four of fp32 where two would take more than 512
+// threads.
 RowPlan bwd_plan(int cols, bool bf) {
     const int vecs = bf ? (cols + 7) / 8 : (cols + 3) / 4;
     return plan_of(vecs, vecs <= 64 ? 1 : bf || vecs <= 1024 ? 2 : 4);

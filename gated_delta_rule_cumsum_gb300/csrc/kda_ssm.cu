@@ -813,7 +813,7 @@ cudaError_t bwd(const SsmArgs &a, cudaStream_t st) {
     if ((e = chunk_states<T, true>(a, st)) != cudaSuccess) return e;
     if ((e = state_pass<true>(a, st)) != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.T;
-    if (a.slots > 0 && a.slots * a.H <= INT32_MAX) {
+    if (a.slots > 0) {  // (slots x H fits a grid: chunk_states has checked it)
         prof_begin("ssm_chunk_grads", st);
         ssm_chunk_grads_kernel<T><<<(unsigned)(a.slots * a.H), 256, kSmemGrads, st>>>(a);
         prof_end(st);
