@@ -8,7 +8,12 @@
 // before), or zero.  2 W flops against 2 elements moved: bandwidth-bound at every size.
 // A thread owns a few adjacent channels and walks down a strip of rows with the last
 // W - 1 rows in registers, so each row is read once (and W - 1 rows more per strip, from
-// L2).  All arithmetic is fp32; outputs are rounded once.
+// L2).  All arithmetic is fp32, in pairs (the packed operations take two values an issue slot);
+// outputs are rounded once.
+//
+// Measured, GB300, 8192 rows x 6144 channels x 4 taps, bf16: forward 37 us (201 MB, 5.4 TB/s),
+// backward 75 us (302 MB, 4.0 TB/s; issue slots 52% busy) and 5 us for the strips' sums.
+// Where rows are not aligned for vectors (6145 channels) 84 and 176 us.
 #include <type_traits>
 
 #include "kda_block.cuh"
@@ -149,7 +154,8 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
 // each other: a ring in shared memory that asynchronous copies fill.  Every thread copies and
 // reads its own channels alone, so nothing but its own copies is waited for.  Rows that are
 // not aligned for copies of four channels come through registers, one group ahead (fp32,
-// 15000 x 1537: 42 us against 57 with copies of 4 bytes; there are none of 2).
+// 15000 x 1537: 42 us against 57 with copies of 4 bytes; there are none of 2).  Groups, 8192 x
+// 6144 bf16: forward 38.4, 36.2 and 37.3 us with 3, 4 and 6; backward 81.7 and 74.2 with 2 and 3.
 template <typename T, bool AL, int U, int GROUPS, int R>
 struct Ahead {
     static constexpr bool kRing = AL;
@@ -478,7 +484,8 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, in
 }
 
 // One token per row.  A thread takes `per` batch rows, four at a time, so that its channels'
-// weights (twice the bytes of a row's state) are read once for all of them.
+// weights (twice the bytes of a row's state) are read once for all of them: 512 x 6144, 11.4 us
+// (25 MB from memory), 27.6 us with one row a thread.
 constexpr int kStepRows = 4;
 template <typename T, int W, bool AL>
 __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvStepArgs p, int per) {
@@ -578,7 +585,9 @@ int64_t channel_blocks(int C) { return (C + kCh * kConvThreads - 1) / (kCh * kCo
 }  // namespace
 
 // Long strips re-read little (W - 1 rows each) and leave few partial sums; short inputs get
-// shorter ones, down to 8 rows, until there are 152 x 1024 threads.
+// shorter ones, down to 8 rows, until there are 152 x 1024 threads (2048 channels: at 512 rows
+// 4.3 us forward and 10.4 us backward against 7.9 and 22.4 with the longest strips, at 64 rows
+// 3.4 and 7.7 against 7.5 and 13.5; at 8192 x 6144 no difference).
 int conv_bwd_strip(int B, int T, int C) { return strip_for((int64_t)B * T, C, 128); }
 
 cudaError_t launch_conv_fwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {

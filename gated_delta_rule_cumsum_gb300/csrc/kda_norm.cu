@@ -8,6 +8,10 @@
 // A row stays in its threads' registers between the sums and the output, so every input
 // is read once and every output written once: bandwidth-bound (2 flops a byte).  The sum
 // h is kept in fp32 for the norm; the stored h is rounded once, beside it.
+//
+// Measured, GB300, bf16: forward 16384 x 2048 43.5 us (268 MB, 6.2 TB/s), 8192 x 4096 to e4m3
+// 48 us (235 MB, 4.9 TB/s); backward 16384 x 2048 52 us (268 MB, 5.2 TB/s).  Rows of 16384
+// columns spill registers in blocks of 1024 threads: 3.8 TB/s forward, 1.7 backward.
 #include <cuda_fp8.h>
 
 #include <algorithm>

@@ -11,7 +11,18 @@
 // dB and dC are summed over a group's heads in tensor memory: a CTA takes a part of a group's
 // units (head, 64 columns) of one chunk, one after another, and leaves one fp32 tile per
 // part; a last kernel adds the parts in order.  What the kernels make themselves goes into
-// the products in two bf16 parts (2^-17); sums, W's and Q's elements are fp32.
+// the products in two bf16 parts (2^-17); sums, W's and Q's elements are fp32.  The states S
+// and E come in two parts as well, and with them u, v: the gradients of A_log and dt_bias, sums
+// over all rows, carry some 2^-18 of the root of the sum of their terms' squares.  A third part
+// would cost half as much again of the states' traffic and room in shared memory that is not
+// there, for inputs of 2^-9.
+//
+// Measured, GB300, 8192 rows, 32 heads of 64, one group, 128 state rows: i side 69 us, j side
+// 105 us.  A unit takes about 8 and 12 thousand cycles, of which its products take a third (the
+// tensor pipe is active 28 to 31% of the time): the rest is the chain from products to
+// factors and back, in warps that can only read their own quarter of the rows, so that one
+// quarter's warps have most of the triangle.  Issuing the next unit's first products ahead of a
+// unit's last ones, and the rows' loads earlier, moved the waits and not the sum (within 2%).
 #include "kda_ssm_tc.cuh"
 
 namespace kda {
@@ -894,7 +905,10 @@ cudaError_t grads(const SsmArgs &a, unsigned blocks, cudaStream_t st) {
 
 }  // namespace
 
-// The split of a group's units that takes the fewest rounds of units on 152 SMs.
+// The split of a group's units that takes the fewest rounds of units on 152 SMs.  64 chunks of
+// one group with 32 units: 2 parts, 358 us for the whole training pass; 1, 4, 5 and 7 parts 511,
+// 380, 429 and 395 us.  Equal stretches over all SMs, across chunks, were slower too: each
+// chunk begins with its B and C and ends with its tile of sums.
 int ssm_tc_parts(int64_t slots, int G, int units) {
     const int64_t items = slots * G;
     if (items == 0 || units <= 1) return 1;
