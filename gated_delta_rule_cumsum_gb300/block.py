@@ -18,8 +18,8 @@ from . import (KDA_DTYPE_BF16, KDA_DTYPE_F32, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUP
                _check, _one_device, _SIGNATURES, load)
 
 __all__ = [
-    "KDA_CONV_FLAG_SILU", "KDA_SSM_FLAG_DT_SOFTPLUS", "KDA_NORM_SAME", "KDA_NORM_E4M3",
-    "KDA_NORM_INT8", "KDA_DEVICE_BAD_INDEX", "KdaConvShape", "KdaSsmShape", "KdaNormShape",
+    "KDA_CONV_FLAG_SILU", "KDA_SSM_FLAG_DT_SOFTPLUS", "KDA_SSM_FLAG_NO_SAVE", "KDA_NORM_SAME",
+    "KDA_NORM_E4M3", "KDA_NORM_INT8", "KDA_DEVICE_BAD_INDEX", "KdaConvShape", "KdaSsmShape", "KdaNormShape",
     "kda_short_conv_fwd", "kda_short_conv_bwd", "kda_short_conv_bwd_workspace_size",
     "kda_short_conv_step", "kda_ssm_scan_fwd", "kda_ssm_scan_bwd", "kda_ssm_workspace_size",
     "kda_ssm_bwd_workspace_size", "kda_ssm_step", "kda_add_rmsnorm_fwd", "kda_add_rmsnorm_bwd",
@@ -30,7 +30,7 @@ __all__ = [
 ]
 
 KDA_CONV_FLAG_SILU = 1 << 0
-KDA_SSM_FLAG_DT_SOFTPLUS = 1 << 0
+KDA_SSM_FLAG_DT_SOFTPLUS, KDA_SSM_FLAG_NO_SAVE = 1 << 0, 1 << 2
 KDA_NORM_SAME, KDA_NORM_E4M3, KDA_NORM_INT8 = 0, 1, 2
 KDA_DEVICE_BAD_INDEX = 1 << 4
 
@@ -411,16 +411,13 @@ def _ssm_setup(x, dt, A_log, Bm, Cm, D, dt_bias, initial_state, cu_seqlens, dt_s
     return (x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu_seqlens), shape
 
 
-@_on_device
-def ssm_scan_forward_save(x, dt, A_log, Bm, Cm, *, D=None, dt_bias=None, dt_softplus=True,
-                          initial_state=None, output_final_state=False, cu_seqlens=None,
-                          workspace=None, dev_status=None, stream=None):
-    """ssm_scan that also returns its workspace, which holds the state at each chunk's start:
-    (y, ht or None, saved).  ssm_scan_backward(..., saved=saved) of the same inputs then does
-    not form the states again."""
+def _ssm_forward(x, dt, A_log, Bm, Cm, D, dt_bias, dt_softplus, initial_state, output_final_state,
+                 cu_seqlens, workspace, dev_status, stream, save):
     _no_grad(x, dt, A_log, Bm, Cm, D, dt_bias, initial_state)
     ins, shape = _ssm_setup(x, dt, A_log, Bm, Cm, D, dt_bias, initial_state, cu_seqlens, dt_softplus,
                             workspace, dev_status)
+    if not save:
+        shape.flags |= KDA_SSM_FLAG_NO_SAVE
     dev = x.device
     y = torch.empty(x.shape, dtype=x.dtype, device=dev)
     ht = (torch.empty((shape.num_seqs, shape.H, shape.N, shape.P), dtype=torch.float32, device=dev)
@@ -431,15 +428,25 @@ def ssm_scan_forward_save(x, dt, A_log, Bm, Cm, *, D=None, dt_bias=None, dt_soft
     return y, ht, workspace
 
 
+@_on_device
+def ssm_scan_forward_save(x, dt, A_log, Bm, Cm, *, D=None, dt_bias=None, dt_softplus=True,
+                          initial_state=None, output_final_state=False, cu_seqlens=None,
+                          workspace=None, dev_status=None, stream=None):
+    """ssm_scan that also returns its workspace, which holds the state at each chunk's start:
+    (y, ht or None, saved).  ssm_scan_backward(..., saved=saved) of the same inputs then does
+    not form the states again."""
+    return _ssm_forward(x, dt, A_log, Bm, Cm, D, dt_bias, dt_softplus, initial_state,
+                        output_final_state, cu_seqlens, workspace, dev_status, stream, True)
+
+
+@_on_device
 def ssm_scan(x, dt, A_log, Bm, Cm, *, D=None, dt_bias=None, dt_softplus=True, initial_state=None,
              output_final_state=False, cu_seqlens=None, workspace=None, dev_status=None, stream=None):
     """The selective state-space scan of x [B, T, H, P] with steps dt [B, T, H], Bm and Cm
     [B, T, G, N] (one type), A_log, D and dt_bias [H] fp32; returns (y [B, T, H, P], ht or
     None).  `initial_state` and ht are [N_seqs, H, N, P] fp32."""
-    return ssm_scan_forward_save(x, dt, A_log, Bm, Cm, D=D, dt_bias=dt_bias, dt_softplus=dt_softplus,
-                                 initial_state=initial_state, output_final_state=output_final_state,
-                                 cu_seqlens=cu_seqlens, workspace=workspace, dev_status=dev_status,
-                                 stream=stream)[:2]
+    return _ssm_forward(x, dt, A_log, Bm, Cm, D, dt_bias, dt_softplus, initial_state,
+                        output_final_state, cu_seqlens, workspace, dev_status, stream, False)[:2]
 
 
 @_on_device
@@ -508,9 +515,12 @@ class _SsmFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu, dt_softplus, save):
         d = [None if t is None else t.detach() for t in (x, dt, A_log, Bm, Cm, D, dt_bias, h0)]
-        y, ht, saved = ssm_scan_forward_save(*d[:5], D=d[5], dt_bias=d[6], dt_softplus=dt_softplus,
-                                             initial_state=d[7], output_final_state=True, cu_seqlens=cu)
-        ctx.saved = saved if save else None
+        kw = dict(D=d[5], dt_bias=d[6], dt_softplus=dt_softplus, initial_state=d[7],
+                  output_final_state=True, cu_seqlens=cu)
+        if save:
+            y, ht, ctx.saved = ssm_scan_forward_save(*d[:5], **kw)
+        else:
+            (y, ht), ctx.saved = ssm_scan(*d[:5], **kw), None
         ctx.dt_softplus = dt_softplus
         ctx.save_for_backward(x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu)
         return y, ht

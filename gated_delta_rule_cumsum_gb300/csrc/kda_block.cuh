@@ -75,6 +75,8 @@ struct SsmArgs {
     int64_t slots;
     float *states;                 // per (slot, head) ssm_state_bytes: the state at each chunk's
                                    // start ([Ns][P] fp32, or the tensor-core path's tiles)
+    void *states_lo;               // tensor-core path: the third tile of each state, for the
+                                   // backward (null: not wanted)
     void *rows;                    // per (slot, head) ssm_rows_bytes: the rows' decays
     float *decay;                  // [slots][H]: each chunk's decay from start to end
     // backward
@@ -83,6 +85,7 @@ struct SsmArgs {
     void *dx, *ddt, *dB, *dC;
     float *dA_log, *dD, *ddt_bias, *dh0;
     float *dstates;                // the state gradient at each chunk's end, as states
+    void *dstates_lo;
     // fp32 path: the heads' shares of dB and dC ([rows][H][Ns]); tensor-core path: those of the
     // parts a group's heads are split in ([slots][G][parts][128][Ns])
     float *dBh, *dCh;
@@ -100,6 +103,7 @@ cudaError_t launch_ssm_bwd(const SsmArgs &a, kda_dtype dt, cudaStream_t st);
 // The tensor-core path (kda_ssm_tc.cu): bf16, Ns a multiple of 8 up to 128, P of 8.
 bool ssm_tc_supported(kda_dtype dt, int Ns, int P);
 size_t ssm_state_bytes(kda_dtype dt, int Ns, int P);
+size_t ssm_state_lo_bytes(kda_dtype dt, int Ns, int P);
 size_t ssm_rows_bytes(kda_dtype dt, int Ns, int P);
 cudaError_t launch_ssm_tc_states(const SsmArgs &a, cudaStream_t st);
 cudaError_t launch_ssm_tc_dstates(const SsmArgs &a, cudaStream_t st);

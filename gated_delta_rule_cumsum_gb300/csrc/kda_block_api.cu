@@ -89,7 +89,7 @@ kda_status check_conv(const char *op, const kda_conv_shape *s, const int32_t *cu
 }
 
 struct SsmWs {
-    size_t ctrl, chunk_start, decay, rows, states, total;
+    size_t ctrl, chunk_start, decay, rows, states, states_lo, total;
 };
 int64_t ssm_slots(const kda_ssm_shape *s, bool packed, int L) {
     const int64_t per = ((int64_t)s->T + L - 1) / L;
@@ -107,11 +107,15 @@ SsmWs ssm_ws(const kda_ssm_shape *s) {
     w.decay = w.chunk_start + kda::align_up(sizeof(int32_t) * ((size_t)s->num_seqs + 1), 256);
     w.rows = kda::align_up(w.decay + (size_t)slots * s->H * 4, 256);
     w.states = kda::align_up(w.rows + (size_t)slots * s->H * kda::ssm_rows_bytes(s->dtype, s->N, s->P), 256);
-    w.total = kda::align_up(w.states + (size_t)slots * s->H * kda::ssm_state_bytes(s->dtype, s->N, s->P), 256);
+    const size_t heads = (size_t)slots * s->H;
+    w.states_lo = kda::align_up(w.states + heads * kda::ssm_state_bytes(s->dtype, s->N, s->P), 256);
+    w.total = kda::align_up(
+        w.states_lo + (s->flags & KDA_SSM_FLAG_NO_SAVE ? 0 : heads * kda::ssm_state_lo_bytes(s->dtype, s->N, s->P)),
+        256);
     return w;
 }
 struct SsmBwdWs {
-    size_t dstates, dBh, dCh, sums, rowg, dDp, es, fwd, total;
+    size_t dstates, dstates_lo, dBh, dCh, sums, rowg, dDp, es, fwd, total;
     int parts;
 };
 SsmBwdWs ssm_bwd_ws(const kda_ssm_shape *s, bool saved) {
@@ -123,7 +127,8 @@ SsmBwdWs ssm_bwd_ws(const kda_ssm_shape *s, bool saved) {
     w.parts = tc ? kda::ssm_tc_parts((int64_t)slots, s->G, (int)(s->H / s->G * tiles)) : 1;
     const size_t share = tc ? slots * s->G * w.parts * L * s->N * 4 : (size_t)s->B * s->T * s->H * s->N * 4;
     w.dstates = 0;
-    w.dBh = kda::align_up(heads * kda::ssm_state_bytes(s->dtype, s->N, s->P), 256);
+    w.dstates_lo = kda::align_up(heads * kda::ssm_state_bytes(s->dtype, s->N, s->P), 256);
+    w.dBh = kda::align_up(w.dstates_lo + heads * kda::ssm_state_lo_bytes(s->dtype, s->N, s->P), 256);
     w.dCh = kda::align_up(w.dBh + share, 256);
     w.sums = kda::align_up(w.dCh + share, 256);
     w.rowg = kda::align_up(w.sums + heads * 3 * 4, 256);
@@ -149,7 +154,7 @@ kda_status check_ssm(const char *op, const kda_ssm_shape *s, const int32_t *cu, 
                     s->G, s->N, s->P);
     if (s->N > 256 || s->P > 256)
         return fail(KDA_ERR_UNSUPPORTED, "%s: N=%d, P=%d (supported: up to 256)", op, s->N, s->P);
-    if (s->flags & ~KDA_SSM_FLAG_DT_SOFTPLUS)
+    if (s->flags & ~(KDA_SSM_FLAG_DT_SOFTPLUS | KDA_SSM_FLAG_NO_SAVE))
         return fail(KDA_ERR_UNSUPPORTED, "%s: unknown flag bits 0x%x", op, s->flags);
     *a = kda::SsmArgs();
     if ((st = check_stride(op, "x_stride", s->x_stride, (int64_t)s->H * s->P, &a->x_stride)) != KDA_OK ||
@@ -174,6 +179,7 @@ void carve_fwd(const kda_ssm_shape *s, char *ws, kda::SsmArgs *a) {
     a->decay = reinterpret_cast<float *>(ws + w.decay);
     a->rows = ws + w.rows;
     a->states = reinterpret_cast<float *>(ws + w.states);
+    a->states_lo = s->flags & KDA_SSM_FLAG_NO_SAVE ? nullptr : ws + w.states_lo;
 }
 
 bool norm_ok(const kda_norm_shape *s) { return s && s->rows >= 0 && s->cols >= 1 && s->cols <= 16384; }
@@ -300,6 +306,8 @@ kda_status kda_ssm_scan_bwd(const void *x, const void *dt, const float *A_log, c
     kda::SsmArgs a;
     kda_status st = check_ssm(op, shape, cu_seqlens, &a);
     if (st != KDA_OK) return st;
+    if (shape->flags & KDA_SSM_FLAG_NO_SAVE)
+        return fail(KDA_ERR_INVALID_ARG, "%s: KDA_SSM_FLAG_NO_SAVE is the forward's alone", op);
     const int64_t rows = (int64_t)a.B * a.T;
     if (!A_log || !dA_log || (rows > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dB || !dC)))
         return fail(KDA_ERR_INVALID_ARG, "%s: x, dt, A_log, Bm, Cm, dy and dx, ddt, dB, dC, dA_log must "
@@ -316,6 +324,7 @@ kda_status kda_ssm_scan_bwd(const void *x, const void *dt, const float *A_log, c
     char *ws = static_cast<char *>(workspace);
     const SsmBwdWs w = ssm_bwd_ws(shape, saved != nullptr);
     a.dstates = reinterpret_cast<float *>(ws + w.dstates);
+    a.dstates_lo = ws + w.dstates_lo;
     a.dBh = reinterpret_cast<float *>(ws + w.dBh);
     a.dCh = reinterpret_cast<float *>(ws + w.dCh);
     a.sums = reinterpret_cast<float *>(ws + w.sums);

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_state_kernel(SsmArgs p) 
 
 // The pass over a sequence's chunks (see ssm_state_pass_kernel), 8 columns of one state row
 // per thread, in the order they lie in memory; the running state stays fp32 and is left at
-// each chunk as hi and lo rows.
+// each chunk as hi and mid rows, and as lo rows where the backward will want them.
 // Measured: the same size, forward 20 us (134 MB, 6.7 TB/s), reverse 38 us (201 MB, 5.3 TB/s).
 template <bool REV>
 __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
@@ -357,7 +357,12 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
             for (int j = 0; j < 8; ++j) run[j] = from[user + j];
         }
     }
-    const int64_t tile = state_tile_bytes(p.Ns), hop = (int64_t)p.H * pt * 2 * tile;
+    const int64_t tile = state_tile_bytes(p.Ns), lo_hop = (int64_t)p.H * pt * tile, hop = 2 * lo_hop;
+    const int64_t lo_at = first * lo_hop + ((int64_t)h * pt + tl) * tile + (int64_t)e * 16;
+    uint8_t *st_lo = static_cast<uint8_t *>(REV ? p.dstates_lo : p.states_lo);
+    const bool keep_lo = st_lo != nullptr;
+    st_lo += lo_at;
+    const uint8_t *sf_lo = static_cast<const uint8_t *>(p.states_lo) + lo_at;
     uint8_t *st = reinterpret_cast<uint8_t *>(REV ? p.dstates : p.states) + first * hop +
                   ((int64_t)h * pt + tl) * 2 * tile + (int64_t)e * 16;
     const float *dec = p.decay + first * p.H + h;
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
     constexpr int U = 4;
     for (int k0 = 0; k0 < nc; k0 += U) {
         float4 own[U][2];
-        uint4 sv[U][2];  // reverse: the states' hi and lo rows
+        uint4 sv[U][3];  // reverse: the states' hi, mid and lo rows
         float dk[U], es4[U] = {};
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -379,6 +384,7 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
                 if constexpr (REV) {
                     sv[u][0] = *reinterpret_cast<const uint4 *>(sf + k * hop);
                     sv[u][1] = *reinterpret_cast<const uint4 *>(sf + k * hop + tile);
+                    sv[u][2] = *reinterpret_cast<const uint4 *>(sf_lo + k * lo_hop);
                 }
                 dk[u] = dec[k * p.H];
             }
@@ -387,19 +393,21 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
             if (k0 + u < nc && live) {
                 const int64_t k = REV ? nc - 1 - (k0 + u) : k0 + u;
                 if constexpr (REV) {
-                    float h8[8], l8[8];
+                    float h8[8], m8[8], l8[8];
                     load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(&sv[u][0]), 8, h8);
-                    load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(&sv[u][1]), 8, l8);
+                    load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(&sv[u][1]), 8, m8);
+                    load_vec<bf16, 8, true>(reinterpret_cast<const bf16 *>(&sv[u][2]), 8, l8);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) es4[u] = fmaf(run[j], h8[j] + l8[j], es4[u]);
+                    for (int j = 0; j < 8; ++j) es4[u] = fmaf(run[j], h8[j] + (m8[j] + l8[j]), es4[u]);
                 }
-                uint4 hi, lo;
-                split2(run[0], run[1], hi.x, lo.x);
-                split2(run[2], run[3], hi.y, lo.y);
-                split2(run[4], run[5], hi.z, lo.z);
-                split2(run[6], run[7], hi.w, lo.w);
+                uint4 hi, mid, lo;
+                split3(run[0], run[1], hi.x, mid.x, lo.x);
+                split3(run[2], run[3], hi.y, mid.y, lo.y);
+                split3(run[4], run[5], hi.z, mid.z, lo.z);
+                split3(run[6], run[7], hi.w, mid.w, lo.w);
                 *reinterpret_cast<uint4 *>(st + k * hop) = hi;
-                *reinterpret_cast<uint4 *>(st + k * hop + tile) = lo;
+                *reinterpret_cast<uint4 *>(st + k * hop + tile) = mid;
+                if (keep_lo) *reinterpret_cast<uint4 *>(st_lo + k * lo_hop) = lo;
                 const float f[8] = {own[u][0].x, own[u][0].y, own[u][0].z, own[u][0].w,
                                     own[u][1].x, own[u][1].y, own[u][1].z, own[u][1].w};
 #pragma unroll
@@ -929,6 +937,9 @@ cudaError_t launch_ssm_tc_out(const SsmArgs &a, cudaStream_t st) {
 size_t ssm_state_bytes(kda_dtype dt, int Ns, int P) {
     return ssm_tc_supported(dt, Ns, P) ? (size_t)(tiles_of(P) * 2 * state_tile_bytes(Ns))
                                        : (size_t)Ns * P * 4;
+}
+size_t ssm_state_lo_bytes(kda_dtype dt, int Ns, int P) {
+    return ssm_tc_supported(dt, Ns, P) ? (size_t)(tiles_of(P) * state_tile_bytes(Ns)) : 0;
 }
 size_t ssm_rows_bytes(kda_dtype dt, int Ns, int P) {
     return ssm_tc_supported(dt, Ns, P) ? sizeof(RowDecays) : 0;

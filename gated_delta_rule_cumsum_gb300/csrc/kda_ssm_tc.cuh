@@ -60,10 +60,12 @@ __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A chunk state of one head and 64 columns lies in memory as the next kernel's operand: two
-// core-matrix tiles of [Ns][64] bf16, hi and then lo, so that one bulk copy each brings it to
-// shared memory.  Byte offset of the 16-byte row of columns 8 g .. 8 g + 7 of state row n in
-// either tile:
+// A chunk state of one head and 64 columns lies in memory as the next kernel's operand:
+// core-matrix tiles of [Ns][64] bf16, so that one bulk copy each brings it to shared memory.  hi
+// and mid (2^-17 of the state) are what y, dB and dC are made of, rounded to bf16 themselves; with
+// lo, in an array of its own, the three are the fp32 state to 2^-25, for the sums behind the
+// fp32 gradients of A_log and dt_bias.  Byte offset of the 16-byte row of columns 8 g .. 8 g + 7
+// of state row n in any tile:
 __host__ __device__ __forceinline__ int64_t state_off(int n, int g) {
     return (int64_t)(n >> 3) * (kPT * 16) + g * 128 + (n & 7) * 16;
 }

@@ -12,10 +12,10 @@
 // units (head, 64 columns) of one chunk, one after another, and leaves one fp32 tile per
 // part; a last kernel adds the parts in order.  What the kernels make themselves goes into
 // the products in two bf16 parts (2^-17); sums, W's and Q's elements are fp32.  The states S
-// and E come in two parts as well, and with them u, v: the gradients of A_log and dt_bias, sums
-// over all rows, carry some 2^-18 of the root of the sum of their terms' squares.  A third part
-// would cost half as much again of the states' traffic and room in shared memory that is not
-// there, for inputs of 2^-9.
+// and E come in three parts (2^-25) where they make u, v and B E, which the fp32 gradients of
+// A_log and dt_bias sum with either sign over all rows: with two parts these were off by 2^-18 of
+// the root of the sum of their terms' squares, 5e-5 of a single head's whose sum cancels.  dB
+// and dC, bf16, take two of the three.
 //
 // Measured, GB300, 8192 rows, 32 heads of 64, one group, 128 state rows: i side 69 us, j side
 // 105 us.  A unit takes about 8 and 12 thousand cycles, of which its products take a third (the
@@ -163,8 +163,9 @@ struct GradISmem {
         uint8_t x[kTL * kPT * 2], dy[kTL * kPT * 2], S[2 * NK * kPT * 2];
         RowDecays dec;
     } st[2];
+    uint8_t S_lo[NK * kPT * 2];
     float rs[4][kTL], rq[4][kTL], us[4][kTL];
-    uint64_t full[2], rows[2], z_done, dy_ready, e_done, w_ready, done, g_done, cb;
+    uint64_t lo_full, full[2], rows[2], z_done, dy_ready, e_done, w_ready, done, g_done, cb;
     uint32_t slot_addr;
     int dead;
 };
@@ -180,6 +181,8 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
     for (int st = 0; st < 2; ++st)  // state rows past Ns are zeros
         for (int e = tid; e < 2 * NK * kPT * 2 / 16; e += kGAll)
             reinterpret_cast<uint4 *>(s.st[st].S)[e] = make_uint4(0u, 0u, 0u, 0u);
+    for (int e = tid; e < NK * kPT * 2 / 16; e += kGAll)
+        reinterpret_cast<uint4 *>(s.S_lo)[e] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) {
         for (int k = 0; k < 2; ++k) {
             tc::mbar_init(&s.full[k], 1);
@@ -189,6 +192,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
         tc::mbar_init(&s.e_done, 1);
         tc::mbar_init(&s.done, 1);
         tc::mbar_init(&s.dy_ready, kGWarps);
+        tc::mbar_init(&s.lo_full, 1);
         tc::mbar_init(&s.w_ready, kGWarps);
         tc::mbar_init(&s.cb, kGWarps);
         tc::mbar_init(&s.g_done, 1);
@@ -215,10 +219,20 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
                 tc::bulk_g2s(&st.dec, static_cast<const RowDecays *>(p.rows) + w.slot * p.H + u.h, sizeof(RowDecays),
                              bar);
             };
+            int fetched_lo = 0;
+            auto fetch_lo = [&](int it) {
+                fetched_lo = it + 1;
+                tc::mbar_arrive_expect_tx(&s.lo_full, (uint32_t)tile);
+                tc::bulk_g2s(s.S_lo, static_cast<const uint8_t *>(p.states_lo) + w.at(p, it).unit * tile, (uint32_t)tile,
+                             &s.lo_full);
+            };
             const uint64_t ck = tc::sdesc(tc::smem_addr(s.C), 128, NK * 16);   // K-major
             const uint64_t bk = tc::sdesc(tc::smem_addr(s.B), 128, NK * 16);
             const uint64_t bmn = tc::sdesc(tc::smem_addr(s.B), NK * 16, 128);  // rows = K
-            if (n > 0) fetch(0);
+            if (n > 0) {
+                fetch(0);
+                fetch_lo(0);
+            }
             if (n > 1) fetch(1);
             bool ok = n > 0 && wait_or_die(&s.cb, 0, dead, p.status);
             tc::tc_fence_after();
@@ -237,12 +251,14 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
                               tc::idesc_bf16(128, 128, false, false), kPT / 16, 0);
                     tc::mma_commit(&s.z_done);
                 }
-                ok = ok && wait_or_die(&s.full[it & 1], ph2, dead, p.status);
+                ok = ok && wait_or_die(&s.full[it & 1], ph2, dead, p.status) &&
+                     wait_or_die(&s.lo_full, ph, dead, p.status);
                 if (ok) {
                     const uint64_t smn = tc::sdesc(sa, kPT * 16, 128);
                     const uint32_t id = tc::idesc_bf16(128, kPT, false, true);
                     mma_steps(E, ck, 16, smn, 2 * kPT, id, NK / 16, 0);
                     mma_steps(E, ck, 16, smn + NK * kPT * 2 / 16, 2 * kPT, id, NK / 16, 1);
+                    mma_steps(E, ck, 16, tc::sdesc(tc::smem_addr(s.S_lo), kPT * 16, 128), 2 * kPT, id, NK / 16, 1);
                     tc::mma_commit(&s.e_done);
                 }
                 ok = ok && wait_or_die(&s.dy_ready, ph, dead, p.status);
@@ -255,6 +271,8 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
                     for (int k = 0; k < kPT / 16; ++k)
                         mma_bf16_ts(dC, DY + 16 * k, sk + NK * kPT * 2 / 16 + 16 * k, id, 1);
                 }
+                // C S was the last reader of lo
+                if (it + 1 < n && wait_or_die(&s.e_done, ph, dead, p.status)) fetch_lo(it + 1);
                 ok = ok && wait_or_die(&s.w_ready, ph, dead, p.status);
                 tc::tc_fence_after();
                 if (ok) {
@@ -264,9 +282,11 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
                 // the stage is free once this unit is multiplied and its rows are read
                 if (it + 2 < n && wait_or_die(&s.done, ph, dead, p.status)) fetch(it + 2);
             }
-            if (*dead)
+            if (*dead) {  // what is on its way lands before the block ends
                 for (int it = max(fetched - 2, 0); it < fetched; ++it)
                     tc::mbar_wait(&s.full[it & 1], (it >> 1) & 1, 10000000ull);
+                if (fetched_lo > 0) tc::mbar_wait(&s.lo_full, (fetched_lo - 1) & 1, 10000000ull);
+            }
         }
         __syncwarp();
     } else {
@@ -450,7 +470,7 @@ template <int NK>
 struct GradJSmem {
     uint8_t C[kTL * NK * 2], B[kTL * NK * 2];
     uint8_t x[2][kTL * kPT * 2], dy[2][kTL * kPT * 2];
-    uint8_t E[2 * NK * kPT * 2];
+    uint8_t E[3 * NK * kPT * 2];    // hi, mid, lo
     uint8_t wx[2][kTL * kPT * 2];   // w x, hi and lo
     RowDecays dec[2];
     float qs[4][kTL], vs[4][kTL], dds[kGWarps];
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
     GradWork w;
     if (!w.start(p)) return;
     const int n = w.count;
-    for (int e = tid; e < 2 * NK * kPT * 2 / 16; e += kGAll)
+    for (int e = tid; e < 3 * NK * kPT * 2 / 16; e += kGAll)
         reinterpret_cast<uint4 *>(s.E)[e] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) {
         for (int k = 0; k < 2; ++k) {
@@ -497,9 +517,11 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
                 const GradUnit u = w.at(p, it);
                 uint64_t *bar = &s.full[it & 1];
                 const uint8_t *src = reinterpret_cast<const uint8_t *>(p.dstates) + u.unit * 2 * tile;
-                tc::mbar_arrive_expect_tx(bar, (uint32_t)(2 * tile + sizeof(RowDecays)));
+                tc::mbar_arrive_expect_tx(bar, (uint32_t)(3 * tile + sizeof(RowDecays)));
                 tc::bulk_g2s(s.E, src, (uint32_t)tile, bar);
                 tc::bulk_g2s(s.E + NK * kPT * 2, src + tile, (uint32_t)tile, bar);
+                tc::bulk_g2s(s.E + 2 * NK * kPT * 2, static_cast<const uint8_t *>(p.dstates_lo) + u.unit * tile,
+                             (uint32_t)tile, bar);
                 tc::bulk_g2s(&s.dec[it & 1], static_cast<const RowDecays *>(p.rows) + w.slot * p.H + u.h,
                              sizeof(RowDecays), bar);
             };
@@ -508,7 +530,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             const uint64_t cmn = tc::sdesc(tc::smem_addr(s.C), NK * 16, 128);  // rows = K
             const uint32_t ea = tc::smem_addr(s.E);
             const uint64_t emn = tc::sdesc(ea, kPT * 16, 128), ek = tc::sdesc(ea, 128, kPT * 16);
-            constexpr uint64_t elo = NK * kPT * 2 / 16;
+            constexpr uint64_t emid = NK * kPT * 2 / 16;
             if (n > 0) fetch(0);
             bool ok = n > 0 && wait_or_die(&s.cb, 0, dead, p.status);
             for (int it = 0; it < n; ++it) {
@@ -526,18 +548,19 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
                 if (ok) {
                     const uint32_t id = tc::idesc_bf16(128, kPT, false, true);
                     mma_steps(XI, bk, 16, emn, 2 * kPT, id, NK / 16, 0);
-                    mma_steps(XI, bk, 16, emn + elo, 2 * kPT, id, NK / 16, 1);
+                    mma_steps(XI, bk, 16, emn + emid, 2 * kPT, id, NK / 16, 1);
+                    mma_steps(XI, bk, 16, emn + 2 * emid, 2 * kPT, id, NK / 16, 1);
                     tc::mma_commit(&s.xi_done);
                 }
                 ok = ok && wait_or_die(&s.wx_ready, ph, dead, p.status);
                 tc::tc_fence_after();
-                if (ok) {  // (hi + lo) E_hi + hi E_lo
+                if (ok) {  // (hi + lo) E_hi + hi E_mid
                     const uint32_t id = tc::idesc_bf16(128, NK, false, false);
                     const uint64_t hi = tc::sdesc(tc::smem_addr(s.wx[0]), 128, kPT * 16);
                     const uint64_t lo = tc::sdesc(tc::smem_addr(s.wx[1]), 128, kPT * 16);
                     mma_steps(dB, hi, 16, ek, 16, id, kPT / 16, it > 0);
                     mma_steps(dB, lo, 16, ek, 16, id, kPT / 16, 1);
-                    mma_steps(dB, hi, 16, ek + elo, 16, id, kPT / 16, 1);
+                    mma_steps(dB, hi, 16, ek + emid, 16, id, kPT / 16, 1);
                     tc::mma_commit(&s.e_done);
                 }
                 ok = ok && wait_or_die(&s.m_ready, ph, dead, p.status);

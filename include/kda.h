@@ -520,6 +520,8 @@ kda_status kda_short_conv_step(const void *x, const float *w, const float *bias,
 /* flags of kda_ssm_shape */
 #define KDA_SSM_FLAG_DT_SOFTPLUS (1u << 0) /* the step is softplus(dt + dt_bias), not
                                               dt + dt_bias                              */
+#define KDA_SSM_FLAG_NO_SAVE (1u << 2)     /* of a forward: its workspace will not be given
+                                              to the backward as `saved`, and is smaller */
 
 typedef struct {
     int32_t B, T, H, G, N, P;   /* H heads in G groups (H % G == 0), N state rows and P
@@ -540,7 +542,8 @@ typedef struct {
  *   h0, ht     [num_seqs, H, N, P] fp32 or NULL, as for kda_chunk_fwd; ht may alias h0
  *   y          [B, T, H, P]; rows outside every sequence are not written
  *   workspace  kda_ssm_workspace_size() bytes, 256-byte aligned.  It holds the state at
- *              each chunk's start on return: kda_ssm_scan_bwd takes it as `saved`.
+ *              each chunk's start on return: kda_ssm_scan_bwd takes it as `saved` (not
+ *              with KDA_SSM_FLAG_NO_SAVE, which leaves out what only the backward reads).
  * Steps that are >= 0 keep every decay <= 1; they are not checked.
  */
 kda_status kda_ssm_scan_fwd(const void *x, const void *dt, const float *A_log, const void *Bm,
@@ -555,6 +558,7 @@ size_t kda_ssm_workspace_size(const kda_ssm_shape *shape);
  * [H] fp32 (dD, ddt_bias may be NULL: not stored); dh0 [num_seqs, H, N, P] fp32 or NULL.
  * dB and dC are summed over a group's heads, the [H] gradients over all tokens, each in a
  * fixed order.  With cu_seqlens, rows outside every sequence are zero.
+ * KDA_SSM_FLAG_NO_SAVE is refused.
  *   saved      the workspace of kda_ssm_scan_fwd for the same inputs and shape, untouched
  *              since, or NULL: the chunk states are formed again
  *   workspace  kda_ssm_bwd_workspace_size(shape, saved != NULL) bytes, 256-byte aligned.

@@ -81,6 +81,17 @@ def test_ssm_refusals(kda, kw, status):
         assert kda.kda_ssm_workspace_size(s) == 0 and kda.kda_ssm_bwd_workspace_size(s, False) == 0
 
 
+def test_ssm_no_save(kda):
+    """A forward whose workspace the backward will not read needs less of it; the backward
+    refuses the flag."""
+    flag = kda.KDA_SSM_FLAG_NO_SAVE
+    keep, drop = (ssm(kda, B=1, T=300, N=16, P=64, dtype=kda.KDA_DTYPE_BF16, flags=f) for f in (1, 1 | flag))
+    assert 0 < kda.kda_ssm_workspace_size(drop) < kda.kda_ssm_workspace_size(keep)
+    said(kda, kda.load().kda_ssm_scan_bwd(FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, None, ctypes.byref(drop),
+                                          FAKE, None, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, FAKE, FAKE,
+                                          1 << 40, None, None), 1)
+
+
 def test_ssm_workspace_refusals(kda):
     s, lib = ssm(kda), kda.load()
     r = ctypes.byref(s)

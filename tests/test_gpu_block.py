@@ -242,6 +242,31 @@ def check_scan(kda, dtype, which, sizes, strong=False):
         assert torch.equal(g[k], again[k]), k
 
 
+@pytest.mark.parametrize("T", [3, 20, 150])
+def test_scan_parameter_gradients_keep_fp32(kda_lib, T):
+    """dA_log and ddt_bias are sums of either sign over rows, state rows and columns, and a few
+    tokens' are mostly made of the chunk states: these have to enter with fp32's digits.  In
+    the 2-norm over 64 heads a sum's own rounding is near 2^-24 a term and the approximate
+    exponentials give 2^-22: 1e-6 leaves a factor of four; states of 17 bits would be past 2e-6."""
+    gen = torch.Generator().manual_seed(T)
+    a = scan_inputs(gen, (1, T), 64, 4, 128, 64, torch.bfloat16)
+    h0, dht = rnd(gen, 1, 64, 128, 64), rnd(gen, 1, 64, 128, 64)
+    dy = rnd(gen, *a["x"].shape, dtype=torch.bfloat16)
+    g = kda_lib.ssm_scan_backward(**a, dy=dy, initial_state=h0, dht=dht)
+    r = ob.ssm_scan_grads(**{k: f64(v) for k, v in a.items()}, dy=f64(dy), h0=f64(h0), dht=f64(dht))
+    for k in ("dA_log", "ddt_bias"):
+        err = np.linalg.norm(f64(g[k]) - r[k]) / np.linalg.norm(r[k])
+        assert err <= 1e-6, f"{k}: {err:.2e}"
+
+
+def test_scan_without_saving_is_the_same(kda_lib):
+    gen = torch.Generator().manual_seed(12)
+    a, h0, cu, _, used = scan_case(gen, "packed", (2, 1, 64, 64), torch.bfloat16, False)
+    y, ht = kda_lib.ssm_scan(**a, initial_state=h0, output_final_state=True, cu_seqlens=cu)
+    ys, hs, _ = kda_lib.ssm_scan_forward_save(**a, initial_state=h0, output_final_state=True, cu_seqlens=cu)
+    assert torch.equal(y[:, :used], ys[:, :used]) and torch.equal(ht, hs)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_scan_without_options(kda_lib, dtype):
     """No D, bias, softplus or initial state; steps that are zero for whole stretches."""
