@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
 // strips in order, so that no result depends on the order of atomics.
 template <typename T, int W, bool AL>
 __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 2 ? 4 : 3) conv_bwd_kernel(ConvArgs p) {
+    follow();
     constexpr int U = 4;
     using Ch = Channels<T, AL>;
     using Rows = Ahead<T, AL, U, 3, 2>;
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(kConvThreads, sizeof(T) == 2 ? 4 : 3) conv_bwd
 // Empty sequences: the carried state passes through, and so does its gradient.
 template <typename T>
 __global__ void __launch_bounds__(128) conv_bwd_empty_kernel(ConvArgs p) {
+    follow();
     const int n = blockIdx.x;
     const bool empty = p.cu ? p.cu[n + 1] <= p.cu[n] : p.T == 0;
     if (!empty) return;
@@ -463,6 +465,7 @@ __global__ void __launch_bounds__(128) conv_bwd_empty_kernel(ConvArgs p) {
 // threads per entry each add every eighth strip, then their sums are added.
 __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float *part, int64_t strips, int C,
                                                            int W, float *dw, float *dbias) {
+    follow();
     __shared__ float red[8][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane, total = (int64_t)(W + 1) * C;
@@ -628,19 +631,16 @@ cudaError_t launch_conv_bwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {
     }
     if (a.dstate_in && a.N > 0 && (a.cu || a.T == 0)) {
         prof_begin("conv_bwd_empty", st);
-        if (dt == KDA_DTYPE_BF16)
-            conv_bwd_empty_kernel<__nv_bfloat16><<<(unsigned)a.N, 128, 0, st>>>(a);
-        else
-            conv_bwd_empty_kernel<float><<<(unsigned)a.N, 128, 0, st>>>(a);
+        err = dt == KDA_DTYPE_BF16 ? launch_after(conv_bwd_empty_kernel<__nv_bfloat16>, a.N, 128, 0, st, a)
+                                   : launch_after(conv_bwd_empty_kernel<float>, a.N, 128, 0, st, a);
         prof_end(st);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        if (err != cudaSuccess) return err;
     }
     const int64_t total = (int64_t)(a.W + 1) * a.C;
     prof_begin("conv_bwd_sum", st);
-    conv_bwd_sum_kernel<<<(unsigned)((total + 31) / 32), 256, 0, st>>>(a.part, a.strips, a.C, a.W,
-                                                                       a.dw, a.dbias);
+    err = launch_after(conv_bwd_sum_kernel, (total + 31) / 32, 256, 0, st, a.part, a.strips, a.C, a.W, a.dw, a.dbias);
     prof_end(st);
-    return cudaGetLastError();
+    return err;
 }
 
 cudaError_t launch_conv_step(const ConvStepArgs &a, kda_dtype dt, cudaStream_t st) {

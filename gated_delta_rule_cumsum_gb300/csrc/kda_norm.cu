@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(MAXT, blocks_per_sm(MAXT, NV)) norm_fwd_kernel
 // what a row costs beside its columns (sums over threads, addresses, a barrier) is shared.
 template <typename T, int VEC, int NV, bool AL, int MAXT, int BLOCKS>
 __global__ void __launch_bounds__(MAXT, BLOCKS) norm_bwd_kernel(NormArgs p, int tpr) {
+    follow();
     __shared__ float red[2][64];
     constexpr int VP = VEC / 2;
     const int rpb = blockDim.x / tpr, tid = threadIdx.x % tpr;
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) norm_bwd_kernel(NormArgs p, int 
 // dw: 32 warps to 32 columns, each adding every 32nd share, then their sums in order.
 __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, int64_t parts, int cols,
                                                             float *dw) {
+    follow();
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
@@ -506,10 +508,10 @@ cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     prof_begin("norm_bwd_sum", st);
-    norm_bwd_sum_kernel<<<(unsigned)((a.cols + 31) / 32), 1024, 0, st>>>(a.part, blocks * r.rpb, a.cols,
-                                                                        a.dw);
+    const cudaError_t e = launch_after(norm_bwd_sum_kernel, (a.cols + 31) / 32, 1024, 0, st, a.part, blocks * r.rpb,
+                                       a.cols, a.dw);
     prof_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace kda

@@ -84,6 +84,7 @@ __device__ __forceinline__ void load_rows(uint8_t *tile, const bf16 *src, int64_
 // Measured: 8192 rows x 32 heads, 5 us; bound by latency.
 constexpr int kRowHeads = 16;
 __global__ void __launch_bounds__(32 * kRowHeads) ssm_tc_rows_kernel(SsmArgs p) {
+    follow();
     __shared__ bf16 dts[kRowHeads][kTL + 4];
     const int hb = (p.H + kRowHeads - 1) / kRowHeads, h0 = (int)(blockIdx.x % hb) * kRowHeads;
     const int64_t slot = blockIdx.x / hb;
@@ -176,7 +177,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_state_kernel(SsmArgs p) 
     const int per_group = p.H / p.G, units = per_group * pt, pairs = (units + 1) / 2;  // of a group
     int64_t at, last;
     work_range(slots_now(p) * p.G * pairs, at, last);
-    if (at >= last) return;
+    if (at >= last) {  // (the chunk table is older than the kernel before)
+        follow();
+        return;
+    }
     const int n = (int)(last - at);
     if (tid == 0) {
         for (int k = 0; k < 2; ++k) {
@@ -187,6 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_state_kernel(SsmArgs p) 
         s.dead = 0;
     }
     const uint32_t tm = tmem_open(&s.slot_addr, 256);
+    follow();
     volatile int *dead = &s.dead;
     if (warp == kRowWarps) {
         if (lane == 0) {
@@ -324,6 +329,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_state_kernel(SsmArgs p) 
 // Measured: the same size, forward 20 us (134 MB, 6.7 TB/s), reverse 38 us (201 MB, 5.3 TB/s).
 template <bool REV>
 __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
+    follow();
     const int pt = tiles_of(p.P), per_tile = p.Ns * 8;
     const int64_t np = (int64_t)p.Ns * p.P;
     const int64_t per = ((int64_t)pt * per_tile + 127) / 128, sh = blockIdx.x / per;
@@ -529,7 +535,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pt = tiles_of(p.P);
     int64_t first, last;
     work_range(slots_now(p) * p.H * pt, first, last);
-    if (first >= last) return;
+    if (first >= last) {  // (the chunk table is older than the kernel before)
+        follow();
+        return;
+    }
     const int n = (int)(last - first);
     // state rows Ns .. NK - 1 of the operand are zeros (the copies bring Ns rows)
     for (int e = tid; e < 2 * 2 * NK * kPT * 2 / 16; e += kOutThreads)
@@ -553,6 +562,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
     }
     tc::fence_async_smem();
     const uint32_t tm = tmem_open(&s.slot_addr, 512);
+    follow();
     const uint32_t G = tm, M = tm + 128, E = tm + 256, I = tm + 320, CT = tm + 384;
     volatile int *dead = &s.dead;
     auto warp_arrive = [&](uint64_t *bar) {  // one arrival per warp
@@ -898,10 +908,15 @@ static cudaError_t tc_states(const SsmArgs &a, cudaStream_t st) {
         prof_begin(BWD ? "ssm_tc_dstate" : "ssm_tc_state", st);
         by_tile(al, a.Ns, [&](auto AL, auto NK) {
             constexpr int MT = NK() >= 64 ? NK() : 64;
-            ssm_tc_state_kernel<AL(), BWD, MT><<<(unsigned)blocks, kTcThreads, state_smem<MT>(), st>>>(a);
+            if constexpr (BWD) {  // the backward's first kernel
+                ssm_tc_state_kernel<AL(), BWD, MT><<<(unsigned)blocks, kTcThreads, state_smem<MT>(), st>>>(a);
+                e = cudaGetLastError();
+            } else {
+                e = launch_after(ssm_tc_state_kernel<AL(), BWD, MT>, blocks, kTcThreads, state_smem<MT>(), st, a);
+            }
         });
         prof_end(st);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
     }
     const int64_t groups = (int64_t)tiles_of(a.P) * a.Ns * 8;
     const int64_t pass = (int64_t)a.N * a.H * ((groups + 127) / 128);
@@ -909,9 +924,10 @@ static cudaError_t tc_states(const SsmArgs &a, cudaStream_t st) {
     if (pass > 0) {
         const int vec = aligned_to(BWD ? a.dht : a.h0, 16) && aligned_to(BWD ? a.dh0 : a.ht, 16);
         prof_begin(BWD ? "ssm_tc_dpass" : "ssm_tc_pass", st);
+        // (plainly: blocks this small, let in early, crowd on the SMs that are free first)
         ssm_tc_pass_kernel<BWD><<<(unsigned)pass, 128, 0, st>>>(a, vec);
-        prof_end(st);
         e = cudaGetLastError();
+        prof_end(st);
     }
     return e;
 }
@@ -921,17 +937,17 @@ cudaError_t launch_ssm_tc_dstates(const SsmArgs &a, cudaStream_t st) { return tc
 
 cudaError_t launch_ssm_tc_out(const SsmArgs &a, cudaStream_t st) {
     int sms = 0;
-    const cudaError_t e = tc_setup(&sms);
+    cudaError_t e = tc_setup(&sms);
     if (e != cudaSuccess) return e;
     const int64_t units = a.slots * a.H * tiles_of(a.P), blocks = units < sms ? units : sms;
     if (units == 0) return cudaSuccess;
     prof_begin("ssm_tc_out", st);
     by_tile(tc_aligned(a), a.Ns, [&](auto AL, auto NK) {
-        ssm_tc_out_kernel<AL(), NK()><<<(unsigned)blocks, kOutThreads, out_smem<NK()>(), st>>>(
-            a, aligned_to(a.y, 16));
+        e = launch_after(ssm_tc_out_kernel<AL(), NK()>, blocks, kOutThreads, out_smem<NK()>(), st, a,
+                         aligned_to(a.y, 16));
     });
     prof_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 size_t ssm_state_bytes(kda_dtype dt, int Ns, int P) {

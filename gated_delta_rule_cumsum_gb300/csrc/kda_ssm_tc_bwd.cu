@@ -176,7 +176,10 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
     GradISmem<NK> &s = *reinterpret_cast<GradISmem<NK> *>(raw_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     GradWork w;
-    if (!w.start(p)) return;
+    if (!w.start(p)) {  // (the chunk table is older than the kernel before)
+        follow();
+        return;
+    }
     const int n = w.count;
     for (int st = 0; st < 2; ++st)  // state rows past Ns are zeros
         for (int e = tid; e < 2 * NK * kPT * 2 / 16; e += kGAll)
@@ -201,6 +204,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
     }
     tc::fence_async_smem();
     const uint32_t tm = tmem_open(&s.slot_addr, 512);
+    follow();
     const uint32_t G = tm, W = tm + 128, dC = tm + 256, E = tm + 384, DY = tm + 448;
     volatile int *dead = &s.dead;
     if (warp == kGWarps) {
@@ -485,7 +489,10 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
     GradJSmem<NK> &s = *reinterpret_cast<GradJSmem<NK> *>(raw_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     GradWork w;
-    if (!w.start(p)) return;
+    if (!w.start(p)) {  // (the chunk table is older than the kernel before)
+        follow();
+        return;
+    }
     const int n = w.count;
     for (int e = tid; e < 3 * NK * kPT * 2 / 16; e += kGAll)
         reinterpret_cast<uint4 *>(s.E)[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -506,6 +513,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
     }
     tc::fence_async_smem();
     const uint32_t tm = tmem_open(&s.slot_addr, 512);
+    follow();
     const uint32_t M = tm, W = tm + 128, dB = tm + 256, DX = tm + 384, XI = tm + 448;
     volatile int *dead = &s.dead;
     if (warp == kGWarps) {
@@ -787,6 +795,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
 
 // ------------------------------------------------- the steps' gradients, per (chunk, head)
 __global__ void __launch_bounds__(kTL) ssm_tc_step_grads_kernel(SsmArgs p) {
+    follow();
     __shared__ float su[4], sv[4], red[3][4];
     const int h = (int)(blockIdx.x % p.H), t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t slot = blockIdx.x / p.H;
@@ -858,6 +867,7 @@ __global__ void __launch_bounds__(kTL) ssm_tc_step_grads_kernel(SsmArgs p) {
 // dB and dC rows of a chunk and group, 16 to a block: the sum of the parts, in their order.
 constexpr int kSumRows = 16;
 __global__ void __launch_bounds__(256) ssm_tc_group_sum_kernel(SsmArgs p) {
+    follow();
     const int64_t sg = blockIdx.x / (kTL / kSumRows);
     const int row0 = (int)(blockIdx.x % (kTL / kSumRows)) * kSumRows;
     const int g = (int)(sg % p.G);
@@ -916,14 +926,14 @@ cudaError_t bwd_setup() {
 template <bool AL, int NK>
 cudaError_t grads(const SsmArgs &a, unsigned blocks, cudaStream_t st) {
     prof_begin("ssm_tc_grad_i", st);
-    ssm_tc_grad_i_kernel<AL, NK><<<blocks, kGAll, at_least(sizeof(GradISmem<NK>)), st>>>(a);
+    cudaError_t e = launch_after(ssm_tc_grad_i_kernel<AL, NK>, blocks, kGAll, at_least(sizeof(GradISmem<NK>)), st, a);
     prof_end(st);
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     prof_begin("ssm_tc_grad_j", st);
-    ssm_tc_grad_j_kernel<AL, NK><<<blocks, kGAll, at_least(sizeof(GradJSmem<NK>)), st>>>(a, aligned_to(a.dx, 16));
+    e = launch_after(ssm_tc_grad_j_kernel<AL, NK>, blocks, kGAll, at_least(sizeof(GradJSmem<NK>)), st, a,
+                     aligned_to(a.dx, 16));
     prof_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -968,13 +978,13 @@ cudaError_t launch_ssm_tc_bwd(const SsmArgs &a, cudaStream_t st) {
         e = al ? grads<true, 128>(a, g, st) : grads<false, 128>(a, g, st);
     if (e != cudaSuccess) return e;
     prof_begin("ssm_tc_step_grads", st);
-    ssm_tc_step_grads_kernel<<<(unsigned)heads, kTL, 0, st>>>(a);
+    e = launch_after(ssm_tc_step_grads_kernel, heads, kTL, 0, st, a);
     prof_end(st);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     prof_begin("ssm_tc_group_sum", st);
-    ssm_tc_group_sum_kernel<<<(unsigned)(a.slots * a.G * (kTL / kSumRows)), 256, 0, st>>>(a);
+    e = launch_after(ssm_tc_group_sum_kernel, a.slots * a.G * (kTL / kSumRows), 256, 0, st, a);
     prof_end(st);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace kda
