@@ -13,7 +13,7 @@
 //
 // Measured, GB300, 8192 rows x 6144 channels x 4 taps, bf16: forward 37 us (201 MB, 5.4 TB/s),
 // backward 75 us (302 MB, 4.0 TB/s; issue slots 52% busy) and 5 us for the strips' sums.
-// Where rows are not aligned for vectors (6145 channels) 84 and 176 us.
+// Where rows are not aligned for vectors (6145 channels) 59 and 120 us.
 #include <type_traits>
 
 #include "kda_block.cuh"
@@ -217,8 +217,9 @@ struct Ahead {
     }
 };
 
+// (Blocks per SM: unaligned bf16, 8192 x 6145, 59 us with six, 86 with what the compiler takes.)
 template <typename T, int W, bool AL>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
+__global__ void __launch_bounds__(kConvThreads, AL || sizeof(T) == 4 ? 0 : 6) conv_fwd_kernel(ConvArgs p) {
     constexpr int U = 4;
     using Ch = Channels<T, AL>;
     using Rows = Ahead<T, AL, U, 4, 1>;
@@ -309,9 +310,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs p) {
 // W - 1 rows before its strip to the strip's last row, holding x and dpre of rows
 // t .. t + W - 1; the row that enters is u = t + W - 1.  dw and dbias take the rows of
 // the strip alone; each strip leaves its sums in p.part and a second kernel adds the
-// strips in order, so that no result depends on the order of atomics.
+// strips in order, so that no result depends on the order of atomics.  (Blocks per SM: four where
+// that leaves registers for all of it; unaligned bf16 would spill: 125 us with three, 185 with four.)
 template <typename T, int W, bool AL>
-__global__ void __launch_bounds__(kConvThreads, sizeof(T) == 2 ? 4 : 3) conv_bwd_kernel(ConvArgs p) {
+__global__ void __launch_bounds__(kConvThreads, AL && sizeof(T) == 2 ? 4 : 3) conv_bwd_kernel(ConvArgs p) {
     follow();
     constexpr int U = 4;
     using Ch = Channels<T, AL>;
