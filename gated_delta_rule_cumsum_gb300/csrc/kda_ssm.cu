@@ -19,8 +19,8 @@
 // This file holds the fp32 kernels on the CUDA cores, for every type and size, and the
 // single-token form.  fp32 throughout, each output rounded once.  bf16 inputs whose columns and
 // state rows allow it take the tensor cores instead (kda_ssm_tc.cu): forward and gradients of
-// 16 sequences of 512 rows, 32 heads of 64, 128 state rows, 364 us there against 2840 us here,
-// and of one sequence of one row 67 against 110.  Here the products are bound by the fp32
+// 16 sequences of 512 rows, 32 heads of 64, 128 state rows, 392 us there against 2830 us here,
+// and of one sequence of one row 63 against 107.  Here the products are bound by the fp32
 // pipe and by shared memory's bandwidth.
 #include "kda_block.cuh"
 
@@ -133,7 +133,6 @@ __device__ __forceinline__ void mm64(float (&acc)[4][4], const float *A, const f
 //   backward (BWD true):  sum_i 2^{a_i} C_i dy_i^T             -> dstates
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(256) ssm_chunk_state_kernel(SsmArgs p) {
-    follow();
     extern __shared__ float sm[];
     float *As = sm, *Bs = sm + kTile, *d = Bs + kTile, *a = d + kL, *lo = a + kL, *wgt = lo + kL;
     const int nt = (p.Ns + kL - 1) / kL, pt = (p.P + kL - 1) / kL;
@@ -188,7 +187,6 @@ __global__ void __launch_bounds__(256) ssm_chunk_state_kernel(SsmArgs p) {
 // ahead of the (serial) multiply-adds.
 template <int VEC, bool REV>
 __global__ void __launch_bounds__(128) ssm_state_pass_kernel(SsmArgs p) {
-    follow();
     const int64_t np = (int64_t)p.Ns * p.P;
     const int64_t blocks_per = (np + 128 * VEC - 1) / (128 * VEC);
     const int64_t sh = blockIdx.x / blocks_per;
@@ -260,7 +258,6 @@ __global__ void __launch_bounds__(128) ssm_state_pass_kernel(SsmArgs p) {
 // One chunk of one head: y, 64 columns at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_chunk_out_kernel(SsmArgs p) {
-    follow();
     extern __shared__ float sm[];
     float *Ct = sm, *Bt = Ct + kTile, *Sx = Bt + kTile, *d = Sx + kTile, *a = d + kL;
     float *lo = a + kL;
@@ -348,7 +345,6 @@ __global__ void __launch_bounds__(256) ssm_chunk_out_kernel(SsmArgs p) {
 // (The quotients are formed without the division.)
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_chunk_grads_kernel(SsmArgs p) {
-    follow();
     extern __shared__ float sm[];
     float *M = sm, *W = M + kTile, *X = W + kTile, *Y = X + kTile, *d = Y + kTile, *a = d + kL;
     float *lo = a + kL, *ea = lo + kL, *el = ea + kL, *l = el + kL, *dd = l + kL, *red = dd + kL;  // red: 16 x 64
@@ -627,7 +623,6 @@ __global__ void __launch_bounds__(256) ssm_chunk_grads_kernel(SsmArgs p) {
 // dB and dC: the sum of a group's heads' shares, in the heads' order.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_group_sum_kernel(SsmArgs p, int64_t rows) {
-    follow();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= rows * p.G * p.Ns) return;
     const int n = (int)(i % p.Ns);
@@ -806,9 +801,9 @@ cudaError_t fwd(const SsmArgs &a, cudaStream_t st) {
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     prof_begin("ssm_chunk_out", st);
-    e = launch_after(ssm_chunk_out_kernel<T>, blocks, 256, kSmemOut, st, a);
+    ssm_chunk_out_kernel<T><<<(unsigned)blocks, 256, kSmemOut, st>>>(a);
     prof_end(st);
-    return e;
+    return cudaGetLastError();
 }
 
 cudaError_t param_sums(const SsmArgs &a, cudaStream_t st) {
@@ -827,16 +822,16 @@ cudaError_t bwd(const SsmArgs &a, cudaStream_t st) {
     const int64_t rows = (int64_t)a.B * a.T;
     if (a.slots > 0) {  // (slots x H fits a grid: chunk_states has checked it)
         prof_begin("ssm_chunk_grads", st);
-        e = launch_after(ssm_chunk_grads_kernel<T>, a.slots * a.H, 256, kSmemGrads, st, a);
+        ssm_chunk_grads_kernel<T><<<(unsigned)(a.slots * a.H), 256, kSmemGrads, st>>>(a);
         prof_end(st);
-        if (e != cudaSuccess) return e;
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     const int64_t elems = rows * a.G * a.Ns;
     if (elems > 0) {
         prof_begin("ssm_group_sum", st);
-        e = launch_after(ssm_group_sum_kernel<T>, (elems + 255) / 256, 256, 0, st, a, rows);
+        ssm_group_sum_kernel<T><<<(unsigned)((elems + 255) / 256), 256, 0, st>>>(a, rows);
         prof_end(st);
-        if (e != cudaSuccess) return e;
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return param_sums(a, st);
 }

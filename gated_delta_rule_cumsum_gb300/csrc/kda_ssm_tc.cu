@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_state_kernel(SsmArgs p) 
 // The pass over a sequence's chunks (see ssm_state_pass_kernel), 8 columns of one state row
 // per thread, in the order they lie in memory; the running state stays fp32 and is left at
 // each chunk as hi and mid rows, and as lo rows where the backward will want them.
-// Measured: the same size, forward 20 us (134 MB, 6.7 TB/s), reverse 38 us (201 MB, 5.3 TB/s).
+// Measured: the same size, forward 16 us (134 MB, part of it in L2), with lo rows 24 us (168 MB,
+// 7.0 TB/s); reverse 42 us (268 MB, 6.4 TB/s).
 template <bool REV>
 __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
     follow();
@@ -863,8 +864,8 @@ bool tc_aligned(const SsmArgs &a) {
 }
 
 // f(aligned, padded state rows): 32, 64 or 128, so that indices are shifts.  8192 rows, 32 heads
-// of 64, forward and gradients: 16 state rows 293 us (301 padded to 128), 64 state rows 316
-// (320); rows of x, B and C that are not aligned for 16-byte copies, 425 us against 358.
+// of 64, forward and gradients: 16 state rows 287 us (321 padded to 128), 64 state rows 315
+// (342); rows of x, B and C that are not aligned for 16-byte copies, 440 us against 387.
 template <typename F>
 void by_tile(bool al, int Ns, F &&f) {
     using std::integral_constant;
