@@ -136,8 +136,9 @@ __device__ __forceinline__ void mma_split(uint32_t d, uint32_t at, uint64_t b, u
     }
 }
 
-// A part's fp32 tile [128][Ns] from tensor memory: lane = row, a quarter of the columns per
-// warp (at least 8).
+// A part's fp32 tile of 128 rows from tensor memory: lane = row, a quarter of the columns per
+// warp (at least 8).  In memory [Ns / 4][128][4], so that a warp's stores are contiguous.
+__device__ __forceinline__ int64_t share_off(int row, int col) { return ((int64_t)(col >> 2) * kTL + row) * 4; }
 template <int NK>
 __device__ __forceinline__ void store_share(float *out, uint32_t tm, int warp, int lane, int Ns) {
     constexpr int W = NK / 4;
@@ -147,9 +148,8 @@ __device__ __forceinline__ void store_share(float *out, uint32_t tm, int warp, i
         float t[8];
         tc::tmem_ld8(tc::tmem_at(tm, quad * 32, c0 + c), t);
         if (c0 + c < Ns) {
-            float *o = out + (int64_t)r * Ns + c0 + c;
-            *reinterpret_cast<float4 *>(o) = make_float4(t[0], t[1], t[2], t[3]);
-            *reinterpret_cast<float4 *>(o + 4) = make_float4(t[4], t[5], t[6], t[7]);
+            *reinterpret_cast<float4 *>(out + share_off(r, c0 + c)) = make_float4(t[0], t[1], t[2], t[3]);
+            *reinterpret_cast<float4 *>(out + share_off(r, c0 + c + 4)) = make_float4(t[4], t[5], t[6], t[7]);
         }
     }
 }
@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(kTL) ssm_tc_step_grads_kernel(SsmArgs p) {
 
 // dB and dC rows of a chunk and group, 16 to a block: the sum of the parts, in their order.
 constexpr int kSumRows = 16;
-__global__ void __launch_bounds__(256) ssm_tc_group_sum_kernel(SsmArgs p) {
+__global__ void __launch_bounds__(256) ssm_tc_group_sum_kernel(SsmArgs p, int aligned) {
     follow();
     const int64_t sg = blockIdx.x / (kTL / kSumRows);
     const int row0 = (int)(blockIdx.x % (kTL / kSumRows)) * kSumRows;
@@ -875,24 +875,29 @@ __global__ void __launch_bounds__(256) ssm_tc_group_sum_kernel(SsmArgs p) {
     if (!tc_find_chunk(p, sg / p.G, c)) return;
     const int64_t tile = (int64_t)kTL * p.Ns;
     const float *b = p.dBh + sg * p.parts * tile, *cc = p.dCh + sg * p.parts * tile;
-    const int per_row = p.Ns / 4;
-    for (int k = threadIdx.x; k < kSumRows * per_row; k += 256) {
-        const int r = row0 + k / per_row, n = k % per_row * 4, e = r * per_row + k % per_row;
-        if (r >= c.nr) break;
-        float4 sb = make_float4(0.f, 0.f, 0.f, 0.f), sc = sb;
+    // eight columns a thread; sixteen lanes take a column's rows
+    for (int k = threadIdx.x; k < kSumRows * (p.Ns / 8); k += 256) {
+        const int r = row0 + k % kSumRows, n = k / kSumRows * 8;
+        if (r >= c.nr) continue;
+        float sb[8] = {}, sc[8] = {};
         for (int q = 0; q < p.parts; ++q) {
-            const float4 x = *reinterpret_cast<const float4 *>(b + q * tile + e * 4);
-            const float4 y = *reinterpret_cast<const float4 *>(cc + q * tile + e * 4);
-            sb.x += x.x; sb.y += x.y; sb.z += x.z; sb.w += x.w;
-            sc.x += y.x; sc.y += y.y; sc.z += y.z; sc.w += y.w;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = q * tile + share_off(r, n + 4 * h);
+                const float4 x = *reinterpret_cast<const float4 *>(b + at);
+                const float4 y = *reinterpret_cast<const float4 *>(cc + at);
+                sb[4 * h] += x.x; sb[4 * h + 1] += x.y; sb[4 * h + 2] += x.z; sb[4 * h + 3] += x.w;
+                sc[4 * h] += y.x; sc[4 * h + 1] += y.y; sc[4 * h + 2] += y.z; sc[4 * h + 3] += y.w;
+            }
         }
         const int64_t at = ((c.r0 + r) * p.G + g) * p.Ns + n;
         bf16 *dB = static_cast<bf16 *>(p.dB) + at, *dC = static_cast<bf16 *>(p.dC) + at;
-        const float fb[4] = {sb.x, sb.y, sb.z, sb.w}, fc[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            dB[q] = __float2bfloat16_rn(fb[q]);
-            dC[q] = __float2bfloat16_rn(fc[q]);
+        if (aligned) {
+            store_vec<bf16, 8, true>(dB, 8, sb);
+            store_vec<bf16, 8, true>(dC, 8, sc);
+        } else {
+            store_vec<bf16, 8, false>(dB, 8, sb);
+            store_vec<bf16, 8, false>(dC, 8, sc);
         }
     }
 }
@@ -982,7 +987,8 @@ cudaError_t launch_ssm_tc_bwd(const SsmArgs &a, cudaStream_t st) {
     prof_end(st);
     if (e != cudaSuccess) return e;
     prof_begin("ssm_tc_group_sum", st);
-    e = launch_after(ssm_tc_group_sum_kernel, a.slots * a.G * (kTL / kSumRows), 256, 0, st, a);
+    e = launch_after(ssm_tc_group_sum_kernel, a.slots * a.G * (kTL / kSumRows), 256, 0, st, a,
+                     aligned_to(a.dB, 16) && aligned_to(a.dC, 16));
     prof_end(st);
     return e;
 }
