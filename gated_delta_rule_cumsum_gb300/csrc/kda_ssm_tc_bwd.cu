@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
             wait_or_die(&s.full[it & 1], ph2, dead, p.status);
             const RowDecays &r = s.dec[it & 1];
+            const float D = p.D ? p.D[u.h] : 0.f;
             {   // w x in two parts: each thread's pieces, rows r0 and r0 + 64
                 const int c8 = (tid >> 3) & 7, r0 = (tid >> 6) * 8 + (tid & 7);
 #pragma unroll
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             float dd = 0.f, vsum = 0.f;
 #pragma unroll
             for (int q = 0; q < 16; ++q) dd = fmaf(xv[q], yv[q], dd);
-            const float wj = r.w[j], D = p.D ? p.D[u.h] : 0.f;
+            const float wj = r.w[j];
             wait_or_die(&s.xi_done, ph, dead, p.status);
             tc::tc_fence_after();
             {
@@ -744,31 +745,42 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             }
             wait_or_die(&s.done, ph, dead, p.status);
             tc::tc_fence_after();
-            {
+            {   // dx over dy's tile, whose readers are through, for stores of whole rows
                 uint32_t e[16];
                 tmem_ld16_nowait(tc::tmem_at(DX, quad * 32, part * 16), e);
                 tmem_wait_ld();
-                float o[16];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) o[q] = yv[q] + __uint_as_float(e[q]);
-                const int col = u.tile * kPT + c16 * 8;
-                bf16 *dx = static_cast<bf16 *>(p.dx) + ((w.c.r0 + j) * p.H + u.h) * p.P + col;
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t off = (uint32_t)((j >> 3) * (kPT * 16) + (c16 + q) * 128 + (j & 7) * 16);
+                    uint32_t o[4];
 #pragma unroll
-                for (int q = 0; q < 16; q += 8) {
-                    float f[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = o[q + k];
-                    if (j < w.c.nr && col + q < p.P) {
-                        if (dx_aligned)
-                            store_vec<bf16, 8, true>(dx + q, 8, f);
-                        else
-                            store_vec<bf16, 8, false>(dx + q, 8, f);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        o[k] = pack_bf16(yv[8 * q + 2 * k] + __uint_as_float(e[8 * q + 2 * k]),
+                                         yv[8 * q + 2 * k + 1] + __uint_as_float(e[8 * q + 2 * k + 1]));
+                    *reinterpret_cast<uint4 *>(s.dy[it & 1] + off) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
             tc::tc_fence_before();  // DX, XI and the rows before the next unit's products
             if (it + 1 < n) warp_arrive(&s.rows[(it + 1) & 1]);
             bar_sync(1, kGThreads);
+            {   // a thread's pieces are those that it loads: no other thread's copy overtakes it
+                const int c8 = (tid >> 3) & 7, r0 = (tid >> 6) * 8 + (tid & 7), col = u.tile * kPT + c8 * 8;
+                bf16 *dx = static_cast<bf16 *>(p.dx) + (w.c.r0 * p.H + u.h) * p.P + col;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int rr = r0 + 64 * k;
+                    const uint8_t *src = s.dy[it & 1] + (rr >> 3) * (kPT * 16) + c8 * 128 + (rr & 7) * 16;
+                    bf16 *dst = dx + (int64_t)rr * p.H * p.P;
+                    if (rr < w.c.nr && col < p.P) {
+                        if (dx_aligned) {
+                            *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(src);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) dst[e] = reinterpret_cast<const bf16 *>(src)[e];
+                        }
+                    }
+                }
+            }
             if (tid < kTL) {
                 float *out = p.rowg + u.unit * 4 * kTL + 2 * kTL;
                 const RowDecays &rr = s.dec[it & 1];
