@@ -17,8 +17,8 @@
 // the root of the sum of their terms' squares, 5e-5 of a single head's whose sum cancels.  dB
 // and dC, bf16, take two of the three.
 //
-// Measured, GB300, 8192 rows, 32 heads of 64, one group, 128 state rows: i side 80 us, j side
-// 111 us (69 and 105 with two-part states).  A unit takes about 8 and 12 thousand cycles, of which
+// Measured, GB300, 8192 rows, 32 heads of 64, one group, 128 state rows: i side 77 us, j side
+// 103 us.  A unit takes about 8 and 12 thousand cycles, of which
 // its products take a third (the tensor pipe is active 28 to 31% of the time): the rest is the chain from products to
 // factors and back, in warps that can only read their own quarter of the rows, so that one
 // quarter's warps have most of the triangle.  Issuing the next unit's first products ahead of a
@@ -956,8 +956,8 @@ cudaError_t grads(const SsmArgs &a, unsigned blocks, cudaStream_t st) {
 }  // namespace
 
 // The split of a group's units that takes the fewest rounds of units on 152 SMs.  64 chunks of
-// one group with 32 units: 2 parts, 387 us for a training pass; 1, 4, 5 and 7 parts 558, 409, 462
-// and 425 us.  Equal stretches over all SMs, across chunks, were slower too: each
+// one group with 32 units: 2 parts, 387 us for a training pass when this was measured; 1, 4, 5 and
+// 7 parts 558, 409, 462 and 425 us.  Equal stretches over all SMs, across chunks, were slower too: each
 // chunk begins with its B and C and ends with its tile of sums.
 int ssm_tc_parts(int64_t slots, int G, int units) {
     const int64_t items = slots * G;
