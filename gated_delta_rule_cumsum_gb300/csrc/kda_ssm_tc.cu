@@ -5,8 +5,10 @@
 // Precision.  x, B and C are bf16 and enter the products exactly.  What the kernel makes
 // itself is split into bf16 parts that are multiplied one after another into the same
 // accumulator: the decay-weighted x of a chunk's state in three (2^-25: the final state is
-// an fp32 output), the masked gram and the state in front of y in two (2^-17: y is rounded
-// to bf16 at the end).  One part alone would put 2^-9 beside y's own rounding.
+// an fp32 output; the smallest part first, since an addition to the full sum may cost it a
+// unit in the last place, however small the addend), the masked gram and the state in front of
+// y in two (2^-17: y is rounded to bf16 at the end).  One part alone would put 2^-9 beside y's
+// own rounding.
 #include "kda_ssm_tc.cuh"
 
 namespace kda {
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_state_kernel(SsmArgs p) 
                 const uint64_t x = tc::sdesc(tc::smem_addr(s.X[k & 1]), 2 * kPT * 16, 128);
                 const uint32_t d = tm + (k & 1) * 128;
 #pragma unroll 1
-                for (int q = 0; q < 3; ++q) mma_steps(d, a, 2 * MT, x + q * part, 4 * kPT, idesc, kTL / 16, q > 0);
+                for (int q = 2; q >= 0; --q) mma_steps(d, a, 2 * MT, x + q * part, 4 * kPT, idesc, kTL / 16, q < 2);
                 tc::mma_commit(&s.done[k & 1]);
             }
         }
@@ -337,7 +339,9 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
     const int64_t id = (blockIdx.x % per) * 128 + threadIdx.x;
     const int e = (int)(id % per_tile), tl = (int)(id / per_tile);
     const int n = (e >> 6) * 8 + (e & 7), g = tl * 8 + ((e >> 3) & 7);
-    const bool live = tl < pt && g * 8 < p.P;
+    // columns past P of the last tile go along: they are zero in what the chunks left, and the
+    // products read every column of every part
+    const bool live = tl < pt, mine = live && g * 8 < p.P;
     if (!REV && !live) return;
     const int h = (int)(sh % p.H), seq = (int)(sh / p.H);
     int64_t first;
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
     float *to = REV ? p.dh0 : p.ht;
     const int64_t user = sh * np + (int64_t)n * p.P + g * 8;
     float run[8] = {};
-    if (from && live) {
+    if (from && mine) {
         if (vec) {
             const float4 x = *reinterpret_cast<const float4 *>(from + user);
             const float4 y = *reinterpret_cast<const float4 *>(from + user + 4);
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(128) ssm_tc_pass_kernel(SsmArgs p, int vec) {
             if (lane < U && k0 + lane < nc) es[(int64_t)(nc - 1 - (k0 + lane)) * p.H * per * 4] = c;
         }
     }
-    if (to && live) {
+    if (to && mine) {
         if (vec) {
             *reinterpret_cast<float4 *>(to + user) = make_float4(run[0], run[1], run[2], run[3]);
             *reinterpret_cast<float4 *>(to + user + 4) = make_float4(run[4], run[5], run[6], run[7]);

@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
                 if (ok) {
                     const uint64_t smn = tc::sdesc(sa, kPT * 16, 128);
                     const uint32_t id = tc::idesc_bf16(128, kPT, false, true);
-                    mma_steps(E, ck, 16, smn, 2 * kPT, id, NK / 16, 0);
+                    mma_steps(E, ck, 16, tc::sdesc(tc::smem_addr(s.S_lo), kPT * 16, 128), 2 * kPT, id, NK / 16, 0);
                     mma_steps(E, ck, 16, smn + NK * kPT * 2 / 16, 2 * kPT, id, NK / 16, 1);
-                    mma_steps(E, ck, 16, tc::sdesc(tc::smem_addr(s.S_lo), kPT * 16, 128), 2 * kPT, id, NK / 16, 1);
+                    mma_steps(E, ck, 16, smn, 2 * kPT, id, NK / 16, 1);
                     tc::mma_commit(&s.e_done);
                 }
                 ok = ok && wait_or_die(&s.dy_ready, ph, dead, p.status);
@@ -555,9 +555,9 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
                 ok = ok && wait_or_die(&s.full[it & 1], ph2, dead, p.status);
                 if (ok) {
                     const uint32_t id = tc::idesc_bf16(128, kPT, false, true);
-                    mma_steps(XI, bk, 16, emn, 2 * kPT, id, NK / 16, 0);
+                    mma_steps(XI, bk, 16, emn + 2 * emid, 2 * kPT, id, NK / 16, 0);
                     mma_steps(XI, bk, 16, emn + emid, 2 * kPT, id, NK / 16, 1);
-                    mma_steps(XI, bk, 16, emn + 2 * emid, 2 * kPT, id, NK / 16, 1);
+                    mma_steps(XI, bk, 16, emn, 2 * kPT, id, NK / 16, 1);
                     tc::mma_commit(&s.xi_done);
                 }
                 ok = ok && wait_or_die(&s.wx_ready, ph, dead, p.status);

@@ -259,6 +259,47 @@ def test_scan_parameter_gradients_keep_fp32(kda_lib, T):
         assert err <= 1e-6, f"{k}: {err:.2e}"
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("which", ["rows", "packed"])
+@pytest.mark.parametrize("sizes", [(4, 2, 80, 48), (2, 1, 16, 32), (2, 1, 128, 200), (3, 1, 64, 64), (3, 1, 20, 33)])
+def test_scan_whatever_the_workspaces_held(kda_lib, dtype, which, sizes):
+    """Workspaces full of NaN (0xff bytes) and of zeros give the same results, bit for bit."""
+    H, G, N, P = sizes
+    gen = torch.Generator().manual_seed(13)
+    a, h0, cu, _, used = scan_case(gen, which, sizes, dtype)
+    B, T = a["x"].shape[:2]
+    dy, dht = rnd(gen, *a["x"].shape, dtype=dtype), rnd(gen, *h0.shape)
+    shape = kda_lib.KdaSsmShape(B, T, H, G, N, P, len(h0), kda_lib.KDA_DTYPE_BF16 if dtype == torch.bfloat16
+                                else kda_lib.KDA_DTYPE_F32, 0, 0, 0, 0, 1)
+    got = []
+    for fill in (0, 255):
+        def filled(n):
+            return torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        y, ht, saved = kda_lib.ssm_scan_forward_save(**a, initial_state=h0, output_final_state=True, cu_seqlens=cu,
+                                                     workspace=filled(kda_lib.kda_ssm_workspace_size(shape)))
+        kw = dict(dy=dy, initial_state=h0, dht=dht, cu_seqlens=cu)
+        g = kda_lib.ssm_scan_backward(**a, **kw, saved=saved,
+                                      workspace=filled(kda_lib.kda_ssm_bwd_workspace_size(shape, True)))
+        f = kda_lib.ssm_scan_backward(**a, **kw, workspace=filled(kda_lib.kda_ssm_bwd_workspace_size(shape, False)))
+        got.append([y[:, :used], ht, *g.values(), *f.values()])
+    for one, other in zip(*got):
+        assert torch.isfinite(one).all() and torch.equal(one, other)
+
+
+def test_other_workspaces_whatever_they_held(kda_lib):
+    gen = torch.Generator().manual_seed(14)
+    x, dy, w = rnd(gen, 2, 37, 24), rnd(gen, 2, 37, 24), rnd(gen, 24, 4)
+    wn, got = rnd(gen, 24), []
+    for fill in (0, 255):
+        ws = torch.full((1 << 22,), fill, dtype=torch.uint8, device="cuda")
+        c = kda_lib.short_conv_backward(x, w, dy, workspace=ws)
+        ws = torch.full((1 << 22,), fill, dtype=torch.uint8, device="cuda")
+        n = kda_lib.add_rms_norm_backward(dy, x, wn, workspace=ws)
+        got.append([c["dx"], c["dweight"], n["dx"], n["dweight"]])
+    for one, other in zip(*got):
+        assert torch.isfinite(one).all() and torch.equal(one, other)
+
+
 def test_scan_without_saving_is_the_same(kda_lib):
     gen = torch.Generator().manual_seed(12)
     a, h0, cu, _, used = scan_case(gen, "packed", (2, 1, 64, 64), torch.bfloat16, False)
