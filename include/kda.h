@@ -624,7 +624,8 @@ size_t kda_add_rmsnorm_bwd_workspace_size(const kda_norm_shape *shape);
 /*
  * kda_read_device_status -- synchronise `stream`, copy the status word to
  * *host_bits (may be NULL) and map it to a status: KDA_OK when no bit is set,
- * KDA_ERR_BAD_CU_SEQLENS or KDA_ERR_TIMEOUT otherwise.  Does not clear it.
+ * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_TIMEOUT or, for KDA_DEVICE_BAD_INDEX,
+ * KDA_ERR_INVALID_ARG otherwise.  Does not clear it.
  */
 kda_status kda_read_device_status(const int32_t *dev_status, int32_t *host_bits,
                                   kda_stream_t stream);
