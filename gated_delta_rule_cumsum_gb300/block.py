@@ -206,19 +206,20 @@ def _rows(t: torch.Tensor, lead: int):
             return t.contiguous(), 0
         want *= size[d]
         cols *= size[d]
-    step = 0
+    step = span = None
     for d in range(lead - 1, -1, -1):
         if size[d] == 1:
             continue
-        if step == 0:
-            step, span = stride[d], stride[d] * size[d]
+        if step is None:
+            step = stride[d]
+            if step < cols:  # broadcast or overlapping rows
+                return t.contiguous(), 0
+            span = step * size[d]
         elif stride[d] != span:
             return t.contiguous(), 0
         else:
             span *= size[d]
-    if step < cols:  # one row, or broadcast rows
-        return t.contiguous(), 0
-    return t, step
+    return (t.contiguous(), 0) if step is None else (t, step)  # None: one row
 
 
 def _on_device(fn):

@@ -149,3 +149,31 @@ def test_rows_are_read_in_place_where_they_can_be(kda):
         assert got.is_contiguous() and step == 0 and torch.equal(got, t)
     some = wide[1:2, ::2]  # one sequence: every second row, evenly spaced
     assert rows(some, 2)[0] is some and rows(some, 2)[1] == 80
+
+
+def test_rows_that_repeat_are_copied(kda):
+    """Rows broadcast along a dimension are not evenly spaced: read in place, row b * T + t of
+    one row per sequence would lie past the tensor's end."""
+    rows = kda.block._rows
+    for shape, full in (((3, 1, 8), (3, 5, 8)), ((1, 5, 8), (3, 5, 8)), ((1, 1, 8), (3, 5, 8)),
+                        ((3, 1, 2, 4), (3, 5, 2, 4)), ((2, 3, 1, 8), (2, 3, 4, 8))):
+        t = torch.arange(float(torch.Size(shape).numel())).view(shape).expand(full)
+        got, step = rows(t, 2)
+        assert got.is_contiguous() and step == 0 and torch.equal(got, t)
+    t = torch.arange(16.).view(2, 8).as_strided((2, 3, 4), (4, 2, 1))  # overlapping rows
+    got, step = rows(t, 2)
+    assert got.is_contiguous() and step == 0 and torch.equal(got, t)
+
+
+def test_rows_in_place_stay_inside_their_tensor(kda):
+    """Whatever the view, what is read in place are exactly its elements."""
+    rows, base = kda.block._rows, torch.arange(4.0 * 6 * 10)
+    checked = 0
+    for size in ((1, 1, 4), (1, 6, 4), (4, 1, 4), (2, 3, 4), (3, 2, 5), (2, 2, 1)):
+        for strides in ((a, b, c) for a in (0, 1, 4, 10, 20, 30, 60) for b in (0, 1, 4, 5, 10, 20) for c in (0, 1, 2)):
+            t = base.as_strided(size, strides)
+            got, step = rows(t, 2)
+            flat = got.as_strided((size[0] * size[1], size[2]), (step or size[2], 1))
+            assert torch.equal(flat, t.reshape(-1, size[2])), (size, strides)
+            checked += got is t
+    assert checked > 20
