@@ -86,8 +86,22 @@ def _s(stream):
             else stream.cuda_stream)
 
 
-def _nbytes(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+def _nbytes(t: Optional[torch.Tensor], name: str = "workspace") -> int:
+    """The bytes that lie behind t's pointer."""
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous: its size is counted in elements")
+    return t.numel() * t.element_size()
+
+
+def _word(t: Optional[torch.Tensor]):
+    """dev_status, of which the kernels write the first four bytes."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() < 1:
+        _bad("dev_status must be an int32 tensor of at least one element")
+    return t.data_ptr()
 
 
 def _bytes(n: int, device) -> torch.Tensor:
@@ -98,7 +112,7 @@ def _bytes(n: int, device) -> torch.Tensor:
 def kda_short_conv_fwd(x, w, bias, state_in, cu_seqlens, shape: KdaConvShape, y, state_out,
                        dev_status=None, stream=None):
     _check(load().kda_short_conv_fwd(_p(x), _p(w), _p(bias), _p(state_in), _p(cu_seqlens),
-                                     ctypes.byref(shape), _p(y), _p(state_out), _p(dev_status),
+                                     ctypes.byref(shape), _p(y), _p(state_out), _word(dev_status),
                                      _s(stream)))
 
 
@@ -107,7 +121,7 @@ def kda_short_conv_bwd(x, w, bias, state_in, cu_seqlens, shape: KdaConvShape, dy
     _check(load().kda_short_conv_bwd(_p(x), _p(w), _p(bias), _p(state_in), _p(cu_seqlens),
                                      ctypes.byref(shape), _p(dy), _p(dstate_out), _p(dx), _p(dw),
                                      _p(dbias), _p(dstate_in), _p(workspace), _nbytes(workspace),
-                                     _p(dev_status), _s(stream)))
+                                     _word(dev_status), _s(stream)))
 
 
 def kda_short_conv_bwd_workspace_size(shape: KdaConvShape) -> int:
@@ -117,7 +131,7 @@ def kda_short_conv_bwd_workspace_size(shape: KdaConvShape) -> int:
 def kda_short_conv_step(x, w, bias, state, state_indices, num_slots: int, shape: KdaConvShape, y,
                         dev_status=None, stream=None):
     _check(load().kda_short_conv_step(_p(x), _p(w), _p(bias), _p(state), _p(state_indices),
-                                      int(num_slots), ctypes.byref(shape), _p(y), _p(dev_status),
+                                      int(num_slots), ctypes.byref(shape), _p(y), _word(dev_status),
                                       _s(stream)))
 
 
@@ -125,7 +139,7 @@ def kda_ssm_scan_fwd(x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu_seqlens, shape: Kd
                      workspace, dev_status=None, stream=None):
     _check(load().kda_ssm_scan_fwd(_p(x), _p(dt), _p(A_log), _p(Bm), _p(Cm), _p(D), _p(dt_bias),
                                    _p(h0), _p(cu_seqlens), ctypes.byref(shape), _p(y), _p(ht),
-                                   _p(workspace), _nbytes(workspace), _p(dev_status), _s(stream)))
+                                   _p(workspace), _nbytes(workspace), _word(dev_status), _s(stream)))
 
 
 def kda_ssm_workspace_size(shape: KdaSsmShape) -> int:
@@ -135,11 +149,13 @@ def kda_ssm_workspace_size(shape: KdaSsmShape) -> int:
 def kda_ssm_scan_bwd(x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu_seqlens, shape: KdaSsmShape, dy, dht,
                      dx, ddt, dB, dC, dA_log, dD, ddt_bias, dh0, saved, workspace, dev_status=None,
                      stream=None):
+    if saved is not None and _nbytes(saved, "saved") < kda_ssm_workspace_size(shape):
+        _bad("saved is smaller than the forward's workspace for this shape")
     _check(load().kda_ssm_scan_bwd(_p(x), _p(dt), _p(A_log), _p(Bm), _p(Cm), _p(D), _p(dt_bias),
                                    _p(h0), _p(cu_seqlens), ctypes.byref(shape), _p(dy), _p(dht),
                                    _p(dx), _p(ddt), _p(dB), _p(dC), _p(dA_log), _p(dD), _p(ddt_bias),
                                    _p(dh0), _p(saved), _p(workspace), _nbytes(workspace),
-                                   _p(dev_status), _s(stream)))
+                                   _word(dev_status), _s(stream)))
 
 
 def kda_ssm_bwd_workspace_size(shape: KdaSsmShape, saved: bool) -> int:
@@ -150,7 +166,7 @@ def kda_ssm_step(x, dt, A_log, Bm, Cm, D, dt_bias, state, state_indices, num_slo
                  shape: KdaSsmShape, y, dev_status=None, stream=None):
     _check(load().kda_ssm_step(_p(x), _p(dt), _p(A_log), _p(Bm), _p(Cm), _p(D), _p(dt_bias),
                                _p(state), _p(state_indices), int(num_slots), ctypes.byref(shape),
-                               _p(y), _p(dev_status), _s(stream)))
+                               _p(y), _word(dev_status), _s(stream)))
 
 
 def kda_add_rmsnorm_fwd(x, residual, w, shape: KdaNormShape, h, y, scale, stream=None):
@@ -462,8 +478,6 @@ def ssm_scan_backward(x, dt, A_log, Bm, Cm, dy, *, D=None, dt_bias=None, dt_soft
                             cu_seqlens, dt_softplus, dy, dht, saved, workspace, dev_status)
     dy = _want("dy", dy.detach(), x.shape, x.dtype)
     dht = _want("dht", dht, (shape.num_seqs, shape.H, shape.N, shape.P), torch.float32)
-    if saved is not None and _nbytes(saved) < kda_ssm_workspace_size(shape):
-        _bad("saved is smaller than the forward's workspace for this shape")
     if workspace is None:
         workspace = _bytes(kda_ssm_bwd_workspace_size(shape, saved is not None), x.device)
     low = dict(dtype=x.dtype, device=x.device)

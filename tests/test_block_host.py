@@ -177,3 +177,47 @@ def test_rows_in_place_stay_inside_their_tensor(kda):
             assert torch.equal(flat, t.reshape(-1, size[2])), (size, strides)
             checked += got is t
     assert checked > 20
+
+
+def strided(n):
+    """n bytes by numel(), 16 behind it."""
+    return torch.zeros(16, dtype=torch.uint8).expand(n // 16, 16)
+
+
+def test_binding_refuses_workspaces_with_less_memory_than_elements(kda):
+    """The size of a workspace is counted in elements: they have to lie back to back."""
+    x, w, rows, half = torch.zeros(1, 8, 16), torch.zeros(16, 4), torch.zeros(4, 16), torch.zeros(16)
+    c, n, s = conv(kda, dtype=0), norm(kda, dtype=0), ssm(kda, dtype=0)
+    xs, dt, bc, A = torch.zeros(1, 8, 4, 8), torch.zeros(1, 8, 4), torch.zeros(1, 8, 2, 16), torch.zeros(4)
+    ins = (xs, dt, A, bc, bc, None, None, None, None, s)
+    outs = (xs, None, xs, dt, bc, bc, A, None, None, None)
+    calls = [
+        lambda ws: kda.kda_short_conv_bwd(x, w, None, None, None, c, x, None, x, w, None, None, ws, stream=FakeStream),
+        lambda ws: kda.kda_add_rmsnorm_bwd(rows, rows, half, None, n, rows, half, ws, stream=FakeStream),
+        lambda ws: kda.kda_ssm_scan_fwd(*ins, xs, None, ws, stream=FakeStream),
+        lambda ws: kda.kda_ssm_scan_bwd(*ins, *outs, None, ws, stream=FakeStream),
+    ]
+    for call in calls:
+        for ws in (strided(1 << 24), torch.zeros(1 << 24, dtype=torch.uint8)[::2]):
+            with pytest.raises(kda.KdaError) as e:
+                call(ws)
+            assert e.value.status == kda.KDA_ERR_INVALID_ARG and "contiguous" in str(e.value)
+    whole = torch.zeros(1 << 24, dtype=torch.uint8)
+    for saved in (strided(1 << 24), whole[:kda.kda_ssm_workspace_size(s) - 1]):
+        with pytest.raises(kda.KdaError) as e:
+            kda.kda_ssm_scan_bwd(*ins, *outs, saved, whole, stream=FakeStream)
+        assert e.value.status == kda.KDA_ERR_INVALID_ARG and "saved" in str(e.value)
+
+
+class FakeStream:
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("word", [torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.int64),
+                                  torch.zeros(0, dtype=torch.int32), torch.zeros(1)])
+def test_binding_refuses_other_status_words(kda, word):
+    """The kernels write four bytes there."""
+    x, w, y = torch.zeros(1, 8, 16), torch.zeros(16, 4), torch.zeros(1, 8, 16)
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_short_conv_fwd(x, w, None, None, None, conv(kda, dtype=0), y, None, word, FakeStream)
+    assert e.value.status == kda.KDA_ERR_INVALID_ARG and "dev_status" in str(e.value)
