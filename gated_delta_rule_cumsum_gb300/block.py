@@ -294,6 +294,33 @@ def _indices(idx: Optional[torch.Tensor], batch: int, slots: int):
         _bad(f"state_indices must be a contiguous int32 vector of {batch} entries")
 
 
+class _FirstOrder(torch.autograd.Function):
+    """The last tensors given, as they are, behind a node that refuses to be differentiated."""
+    @staticmethod
+    def forward(ctx, made_from, *ts):
+        return tuple(t.view_as(t) for t in ts[made_from:])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise KdaError(KDA_ERR_UNSUPPORTED, "second-order gradients through the recurrent block's operators")
+
+
+def _first_order(backward):
+    """A backward whose gradients, asked for with create_graph=True, raise when they are
+    differentiated: without a node between them and what they are made of they would pass for
+    constants."""
+    @functools.wraps(backward)
+    def wrapper(ctx, *douts):
+        with torch.no_grad():
+            out = backward(ctx, *douts)
+        if not torch.is_grad_enabled():
+            return out
+        of = [t for t in (*ctx.saved_tensors, *douts) if t is not None and t.requires_grad]
+        kept = iter(_FirstOrder.apply(len(of), *of, *[g for g in out if g is not None]))
+        return tuple(None if g is None else next(kept) for g in out)
+    return wrapper
+
+
 # ------------------------------------------------------- short convolution
 def _conv_setup(x, weight, bias, initial_state, cu_seqlens, activation, *more):
     _same_device(x, weight, bias, initial_state, cu_seqlens, *more)
@@ -390,6 +417,7 @@ class _ConvFunction(torch.autograd.Function):
         return y, end
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dend):
         x, weight, bias, state, cu = ctx.saved_tensors
         g = short_conv_backward(x, weight, dy, bias, initial_state=state, dfinal_state=dend,
@@ -541,6 +569,7 @@ class _SsmFunction(torch.autograd.Function):
         return y, ht
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dht):
         x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu = ctx.saved_tensors
         g = ssm_scan_backward(x, dt, A_log, Bm, Cm, dy, D=D, dt_bias=dt_bias,
@@ -626,11 +655,12 @@ class _NormFunction(torch.autograd.Function):
     def forward(ctx, x, weight, residual, eps):
         y, h = add_rms_norm(x.detach(), weight.detach(),
                             residual=None if residual is None else residual.detach(), eps=eps)
-        ctx.save_for_backward(h, weight)
+        ctx.save_for_backward(x if residual is None else h, weight)
         ctx.eps, ctx.has_res = eps, residual is not None
         return y, h.view_as(h) if residual is None else h
 
     @staticmethod
+    @_first_order
     def backward(ctx, dy, dh):
         h, weight = ctx.saved_tensors
         g = add_rms_norm_backward(dy, h, weight, eps=ctx.eps, dresidual=dh)
