@@ -560,21 +560,22 @@ class _SsmFunction(torch.autograd.Function):
         d = [None if t is None else t.detach() for t in (x, dt, A_log, Bm, Cm, D, dt_bias, h0)]
         kw = dict(D=d[5], dt_bias=d[6], dt_softplus=dt_softplus, initial_state=d[7],
                   output_final_state=True, cu_seqlens=cu)
+        saved = None
         if save:
-            y, ht, ctx.saved = ssm_scan_forward_save(*d[:5], **kw)
+            y, ht, saved = ssm_scan_forward_save(*d[:5], **kw)
         else:
-            (y, ht), ctx.saved = ssm_scan(*d[:5], **kw), None
+            y, ht = ssm_scan(*d[:5], **kw)
         ctx.dt_softplus = dt_softplus
-        ctx.save_for_backward(x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu)
+        ctx.save_for_backward(x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu, saved)
         return y, ht
 
     @staticmethod
     @_first_order
     def backward(ctx, dy, dht):
-        x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu = ctx.saved_tensors
+        x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu, saved = ctx.saved_tensors
         g = ssm_scan_backward(x, dt, A_log, Bm, Cm, dy, D=D, dt_bias=dt_bias,
                               dt_softplus=ctx.dt_softplus, initial_state=h0, dht=dht, cu_seqlens=cu,
-                              saved=ctx.saved)
+                              saved=saved)
         return (g["dx"], g["ddt"], g["dA_log"], g["dB"], g["dC"], g["dD"], g["ddt_bias"], g["dh0"],
                 None, None, None)
 

@@ -88,3 +88,32 @@ def test_first_order_gradients_stay_as_they_were(kda, which):
         got.append(torch.autograd.grad((y * y).sum(), (x, w), create_graph=create))
         assert all(g.requires_grad == create for g in got[-1])
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_chunk_states_are_saved_like_every_tensor(kda):
+    """Hooks on saved tensors (checkpointing, offloading) see them, and they go with the graph's
+    other tensors once the backward has run."""
+    x, A, z = torch.ones(2, 3, requires_grad=True), torch.ones(3, requires_grad=True), torch.zeros(1)
+    seen = []
+
+    def pack(t):
+        seen.append(t.dtype)
+        return t.clone()
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        y, _ = kda.ssm_scan_autograd(x, z, A, z, z)
+    assert torch.uint8 in seen
+    node = y.grad_fn
+    y.sum().backward(retain_graph=True)
+    y.sum().backward()  # the same states twice
+    states = [kw["saved"] for name, kw in kda.log if name == "scan_bwd"]
+    assert len(states) == 2 and all(torch.equal(t, torch.arange(64, dtype=torch.uint8)) for t in states)
+    assert not [v for v in vars(node).values() if isinstance(v, torch.Tensor)]
+    with pytest.raises(RuntimeError):
+        node.saved_tensors
+
+
+def test_no_chunk_states_without_saving(kda):
+    x, A, z = torch.ones(2, 3, requires_grad=True), torch.ones(3, requires_grad=True), torch.zeros(1)
+    kda.ssm_scan_autograd(x, z, A, z, z, save_for_backward=False)[0].sum().backward()
+    assert [kw["saved"] for name, kw in kda.log if name == "scan_bwd"] == [None]
