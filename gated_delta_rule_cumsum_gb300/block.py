@@ -408,12 +408,12 @@ def short_conv_step(x, state, weight, bias=None, *, state_indices=None, activati
 
 class _ConvFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, state, cu, activation):
+    def forward(ctx, x, weight, bias, state, cu, activation, dev_status):
         d = [None if t is None else t.detach() for t in (x, weight, bias, state)]
         y, end = short_conv(d[0], d[1], d[2], initial_state=d[3], output_final_state=True,
-                            cu_seqlens=cu, activation=activation)
+                            cu_seqlens=cu, activation=activation, dev_status=dev_status)
         ctx.save_for_backward(x, weight, bias, state, cu)
-        ctx.activation = activation
+        ctx.activation, ctx.dev_status = activation, dev_status
         return y, end
 
     @staticmethod
@@ -421,15 +421,15 @@ class _ConvFunction(torch.autograd.Function):
     def backward(ctx, dy, dend):
         x, weight, bias, state, cu = ctx.saved_tensors
         g = short_conv_backward(x, weight, dy, bias, initial_state=state, dfinal_state=dend,
-                                cu_seqlens=cu, activation=ctx.activation)
-        return g["dx"], g["dweight"], g["dbias"], g["dinitial_state"], None, None
+                                cu_seqlens=cu, activation=ctx.activation, dev_status=ctx.dev_status)
+        return g["dx"], g["dweight"], g["dbias"], g["dinitial_state"], None, None, None
 
 
 def short_conv_autograd(x, weight, bias=None, *, initial_state=None, cu_seqlens=None,
-                        activation="silu"):
+                        activation="silu", dev_status=None):
     """short_conv behind torch.autograd: (y, final state), with gradients to x, weight, bias
-    and the initial state."""
-    return _ConvFunction.apply(x, weight, bias, initial_state, cu_seqlens, activation)
+    and the initial state.  `dev_status` is given to the forward and to the backward."""
+    return _ConvFunction.apply(x, weight, bias, initial_state, cu_seqlens, activation, dev_status)
 
 
 # ------------------------------------------------------------------ the scan
@@ -556,16 +556,16 @@ def ssm_step(x, dt, A_log, Bm, Cm, state, *, D=None, dt_bias=None, dt_softplus=T
 
 class _SsmFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu, dt_softplus, save):
+    def forward(ctx, x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu, dt_softplus, save, dev_status):
         d = [None if t is None else t.detach() for t in (x, dt, A_log, Bm, Cm, D, dt_bias, h0)]
         kw = dict(D=d[5], dt_bias=d[6], dt_softplus=dt_softplus, initial_state=d[7],
-                  output_final_state=True, cu_seqlens=cu)
+                  output_final_state=True, cu_seqlens=cu, dev_status=dev_status)
         saved = None
         if save:
             y, ht, saved = ssm_scan_forward_save(*d[:5], **kw)
         else:
             y, ht = ssm_scan(*d[:5], **kw)
-        ctx.dt_softplus = dt_softplus
+        ctx.dt_softplus, ctx.dev_status = dt_softplus, dev_status
         ctx.save_for_backward(x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu, saved)
         return y, ht
 
@@ -575,18 +575,19 @@ class _SsmFunction(torch.autograd.Function):
         x, dt, A_log, Bm, Cm, D, dt_bias, h0, cu, saved = ctx.saved_tensors
         g = ssm_scan_backward(x, dt, A_log, Bm, Cm, dy, D=D, dt_bias=dt_bias,
                               dt_softplus=ctx.dt_softplus, initial_state=h0, dht=dht, cu_seqlens=cu,
-                              saved=saved)
+                              saved=saved, dev_status=ctx.dev_status)
         return (g["dx"], g["ddt"], g["dA_log"], g["dB"], g["dC"], g["dD"], g["ddt_bias"], g["dh0"],
-                None, None, None)
+                None, None, None, None)
 
 
 def ssm_scan_autograd(x, dt, A_log, Bm, Cm, *, D=None, dt_bias=None, dt_softplus=True,
-                      initial_state=None, cu_seqlens=None, save_for_backward=True):
+                      initial_state=None, cu_seqlens=None, save_for_backward=True, dev_status=None):
     """ssm_scan behind torch.autograd: (y, ht), with gradients to every floating input.  With
     `save_for_backward` the chunk states are kept from the forward to the backward
-    (kda_ssm_workspace_size bytes); False forms them again."""
+    (kda_ssm_workspace_size bytes); False forms them again.  `dev_status` is given to the
+    forward and to the backward."""
     return _SsmFunction.apply(x, dt, A_log, Bm, Cm, D, dt_bias, initial_state, cu_seqlens,
-                              bool(dt_softplus), bool(save_for_backward))
+                              bool(dt_softplus), bool(save_for_backward), dev_status)
 
 
 # ------------------------------------------------------------------ the norm

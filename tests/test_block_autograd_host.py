@@ -117,3 +117,14 @@ def test_no_chunk_states_without_saving(kda):
     x, A, z = torch.ones(2, 3, requires_grad=True), torch.ones(3, requires_grad=True), torch.zeros(1)
     kda.ssm_scan_autograd(x, z, A, z, z, save_for_backward=False)[0].sum().backward()
     assert [kw["saved"] for name, kw in kda.log if name == "scan_bwd"] == [None]
+
+
+def test_status_words_reach_both_directions(kda):
+    """Bad offsets and waits that ran out can be read after the forward and after the backward."""
+    st = torch.zeros(1, dtype=torch.int32)
+    x, w, z = torch.ones(2, 3, requires_grad=True), torch.ones(3, requires_grad=True), torch.zeros(1)
+    kda.short_conv_autograd(x, w, dev_status=st)[0].sum().backward()
+    kda.ssm_scan_autograd(x, z, w, z, z, dev_status=st)[0].sum().backward()
+    kda.short_conv_autograd(x, w)[0].sum().backward()
+    assert [(name, kw.get("dev_status") is st) for name, kw in kda.log] == [
+        ("conv", True), ("conv_bwd", True), ("scan", True), ("scan_bwd", True), ("conv", False), ("conv_bwd", False)]
