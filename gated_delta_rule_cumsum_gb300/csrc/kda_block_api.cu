@@ -39,6 +39,9 @@ kda_status check_dtype(const char *op, int dt) {
     return KDA_OK;
 }
 
+// All rows of a call, and those rows rounded up to whole chunks, are counted in 32 bits.
+bool rows_ok(int B, int T) { return (int64_t)B * T <= INT_MAX - 255; }
+
 // The batch of a conv or scan shape: dense (num_seqs == B) or packed (B == 1).
 kda_status check_batch(const char *op, int B, int T, int num_seqs, const int32_t *cu) {
     if (B <= 0 || T < 0) return fail(KDA_ERR_INVALID_ARG, "%s: B=%d T=%d", op, B, T);
@@ -51,7 +54,7 @@ kda_status check_batch(const char *op, int B, int T, int num_seqs, const int32_t
         return fail(KDA_ERR_INVALID_ARG, "%s: num_seqs=%d must equal B=%d without cu_seqlens", op,
                     num_seqs, B);
     }
-    if ((double)B * T > INT_MAX) return fail(KDA_ERR_UNSUPPORTED, "%s: too many rows", op);
+    if (!rows_ok(B, T)) return fail(KDA_ERR_UNSUPPORTED, "%s: too many rows", op);
     return KDA_OK;
 }
 
@@ -140,7 +143,7 @@ SsmBwdWs ssm_bwd_ws(const kda_ssm_shape *s, bool saved) {
 }
 
 bool ssm_sizes_ok(const kda_ssm_shape *s) {
-    return s && s->B > 0 && s->T >= 0 && s->H > 0 && s->G > 0 && s->H % s->G == 0 && s->N > 0 &&
+    return s && s->B > 0 && s->T >= 0 && rows_ok(s->B, s->T) && s->H > 0 && s->G > 0 && s->H % s->G == 0 && s->N > 0 &&
            s->N <= 256 && s->P > 0 && s->P <= 256 && s->num_seqs >= 0;
 }
 

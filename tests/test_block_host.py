@@ -221,3 +221,15 @@ def test_binding_refuses_other_status_words(kda, word):
     with pytest.raises(kda.KdaError) as e:
         kda.kda_short_conv_fwd(x, w, None, None, None, conv(kda, dtype=0), y, None, word, FakeStream)
     assert e.value.status == kda.KDA_ERR_INVALID_ARG and "dev_status" in str(e.value)
+
+
+@pytest.mark.parametrize("T", [2**31 - 1, 2**31 - 128, 2**31 - 255])
+def test_ssm_refuses_row_counts_whose_chunk_count_overflows(kda, T):
+    """Kernels round rows up to whole chunks (up to 128) in 32 bits."""
+    s, lib = ssm(kda, T=T, H=1, G=1, N=8, P=8), kda.load()
+    r = ctypes.byref(s)
+    assert kda.kda_ssm_workspace_size(s) == 0 and kda.kda_ssm_bwd_workspace_size(s, False) == 0
+    said(kda, lib.kda_ssm_scan_fwd(FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None, None, r, FAKE, None, FAKE, 0, None,
+                                   None), 2)
+    ok = ssm(kda, T=2**31 - 256, H=1, G=1, N=8, P=8)
+    assert kda.kda_ssm_workspace_size(ok) > 0
