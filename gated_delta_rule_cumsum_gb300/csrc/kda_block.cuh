@@ -141,8 +141,10 @@ __device__ __forceinline__ void follow() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
+// launch_next: `first` where no kernel of the call has been launched before.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, unsigned threads, size_t smem, cudaStream_t st, A... args) {
+cudaError_t launch_next(bool first, void (*kernel)(P...), int64_t blocks, unsigned threads, size_t smem, cudaStream_t st,
+                        A... args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -152,10 +154,14 @@ cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, unsigned threads,
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = first ? 0 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
     if (e != cudaSuccess) cudaGetLastError();  // reported by the return value alone
     return e;
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), int64_t blocks, unsigned threads, size_t smem, cudaStream_t st, A... args) {
+    return launch_next(false, kernel, blocks, threads, smem, st, args...);
 }
 
 // ---------------------------------------------------------------------- helpers

@@ -623,6 +623,7 @@ cudaError_t launch_conv_bwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {
     const int64_t blocks = channel_blocks(a.C) * a.strips;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     cudaError_t err = cudaSuccess;
+    bool first = blocks == 0;  // no kernel of this call so far
     if (blocks > 0) {
         prof_begin("conv_bwd", st);
         err = by_kind(dt, a.W, al, [&](auto t, auto W, auto AL) {
@@ -633,14 +634,16 @@ cudaError_t launch_conv_bwd(ConvArgs a, kda_dtype dt, cudaStream_t st) {
     }
     if (a.dstate_in && a.N > 0 && (a.cu || a.T == 0)) {
         prof_begin("conv_bwd_empty", st);
-        err = dt == KDA_DTYPE_BF16 ? launch_after(conv_bwd_empty_kernel<__nv_bfloat16>, a.N, 128, 0, st, a)
-                                   : launch_after(conv_bwd_empty_kernel<float>, a.N, 128, 0, st, a);
+        err = dt == KDA_DTYPE_BF16 ? launch_next(first, conv_bwd_empty_kernel<__nv_bfloat16>, a.N, 128, 0, st, a)
+                                   : launch_next(first, conv_bwd_empty_kernel<float>, a.N, 128, 0, st, a);
         prof_end(st);
+        first = false;
         if (err != cudaSuccess) return err;
     }
     const int64_t total = (int64_t)(a.W + 1) * a.C;
     prof_begin("conv_bwd_sum", st);
-    err = launch_after(conv_bwd_sum_kernel, (total + 31) / 32, 256, 0, st, a.part, a.strips, a.C, a.W, a.dw, a.dbias);
+    err = launch_next(first, conv_bwd_sum_kernel, (total + 31) / 32, 256, 0, st, a.part, a.strips, a.C, a.W, a.dw,
+                      a.dbias);
     prof_end(st);
     return err;
 }

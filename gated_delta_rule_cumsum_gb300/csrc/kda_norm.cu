@@ -508,8 +508,8 @@ cudaError_t launch_norm_bwd(const NormArgs &a, kda_dtype dt, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     prof_begin("norm_bwd_sum", st);
-    const cudaError_t e = launch_after(norm_bwd_sum_kernel, (a.cols + 31) / 32, 1024, 0, st, a.part, blocks * r.rpb,
-                                       a.cols, a.dw);
+    const cudaError_t e = launch_next(blocks == 0, norm_bwd_sum_kernel, (a.cols + 31) / 32, 1024, 0, st, a.part,
+                                      blocks * r.rpb, a.cols, a.dw);
     prof_end(st);
     return e;
 }

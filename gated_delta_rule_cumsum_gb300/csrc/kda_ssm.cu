@@ -808,7 +808,8 @@ cudaError_t fwd(const SsmArgs &a, cudaStream_t st) {
 
 cudaError_t param_sums(const SsmArgs &a, cudaStream_t st) {
     prof_begin("ssm_param_sum", st);
-    const cudaError_t e = launch_after(ssm_param_sum_kernel, (3 * a.H + 3) / 4, 128, 0, st, a);
+    const bool first = a.slots == 0 && a.N == 0;  // neither chunks nor states
+    const cudaError_t e = launch_next(first, ssm_param_sum_kernel, (3 * a.H + 3) / 4, 128, 0, st, a);
     prof_end(st);
     return e;
 }
