@@ -234,7 +234,7 @@ __device__ __forceinline__ void store_vec(T *p, int n, const float (&v)[VEC]) {
         if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
-            __nv_bfloat162 h[VEC / 2];
+            alignas(2 * VEC) __nv_bfloat162 h[VEC / 2];
 #pragma unroll
             for (int i = 0; i < VEC / 2; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             if constexpr (VEC == 8)

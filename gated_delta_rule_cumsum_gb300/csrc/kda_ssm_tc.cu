@@ -70,7 +70,7 @@ __device__ __forceinline__ void load_rows(uint8_t *tile, const bf16 *src, int64_
         if constexpr (AL) {
             cp_async16(tc::smem_addr(tile) + at, in ? s + k * STEP * stride : src, in);
         } else {
-            bf16 v[8];
+            alignas(16) bf16 v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = in && c8 * 8 + j < nc ? s[k * STEP * stride + j] : __float2bfloat16_rn(0.f);
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) ssm_tc_state_kernel(SsmArgs p) 
                     if constexpr (AL) {
                         xr[k] = *reinterpret_cast<const uint4 *>(v + 32 * k * vs);
                     } else {
-                        bf16 e[8];
+                        alignas(16) bf16 e[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) e[j] = v[32 * k * vs + j];
                         xr[k] = *reinterpret_cast<const uint4 *>(e);
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
                 if constexpr (AL) {
                     cp_async16(tc::smem_addr(dst) + 2 * k * kPT * 16, in ? from : static_cast<const bf16 *>(p.x), in);
                 } else {
-                    bf16 v[8];
+                    alignas(16) bf16 v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = in ? from[j] : __float2bfloat16_rn(0.f);
                     *reinterpret_cast<uint4 *>(dst + 2 * k * kPT * 16) = *reinterpret_cast<const uint4 *>(v);
@@ -714,7 +714,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) ssm_tc_out_kernel(SsmArgs p, i
                 tc::fence_async_smem();
                 bar_sync(5, kRowThreads);
                 if (part < NK / 32) {  // 32 columns of C's rows, in pairs
-                    uint32_t o[16];
+                    alignas(16) uint32_t o[16];
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         *reinterpret_cast<uint4 *>(&o[4 * q]) = *reinterpret_cast<const uint4 *>(

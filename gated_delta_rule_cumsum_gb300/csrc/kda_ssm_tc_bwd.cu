@@ -79,7 +79,7 @@ __device__ __forceinline__ void load_tile64(uint8_t *tile, const bf16 *src, int6
         if constexpr (AL) {
             cp_async16(tc::smem_addr(dst), in ? s : src, in);
         } else {
-            bf16 v[8];
+            alignas(16) bf16 v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = in ? s[j] : __float2bfloat16_rn(0.f);
             *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(v);
@@ -100,7 +100,7 @@ __device__ __forceinline__ void load_wide(uint8_t *tile, const bf16 *src, int64_
         if constexpr (AL) {
             cp_async16(tc::smem_addr(dst), in ? s : src, in);
         } else {
-            bf16 v[8];
+            alignas(16) bf16 v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = in && c8 * 8 + j < nc ? s[j] : __float2bfloat16_rn(0.f);
             *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(v);
