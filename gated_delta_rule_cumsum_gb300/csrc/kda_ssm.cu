@@ -36,7 +36,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Chunk {
     int64_t r0;   // its first row, of all B * T
     int nr;       // rows
-    int seq;
 };
 __device__ __forceinline__ bool find_chunk(const SsmArgs &p, int64_t slot, Chunk &c) {
     if (p.cu) {
@@ -45,12 +44,11 @@ __device__ __forceinline__ bool find_chunk(const SsmArgs &p, int64_t slot, Chunk
         const int s = p.cu[n] + p.L * ((int)slot - p.chunk_start[n]);
         c.r0 = s;
         c.nr = min(p.L, p.cu[n + 1] - s);
-        c.seq = n;
     } else {
         const int per = (p.T + p.L - 1) / p.L;
-        c.seq = (int)(slot / per);
+        const int seq = (int)(slot / per);
         const int k = (int)(slot % per);
-        c.r0 = (int64_t)c.seq * p.T + (int64_t)k * p.L;
+        c.r0 = (int64_t)seq * p.T + (int64_t)k * p.L;
         c.nr = min(p.L, p.T - k * p.L);
     }
     return c.nr > 0;

@@ -17,7 +17,7 @@ constexpr uint64_t kSsmWaitNs = 1000000000ull;
 
 struct TcChunk {
     int64_t r0;
-    int nr, seq;
+    int nr;
 };
 __device__ __forceinline__ bool tc_find_chunk(const SsmArgs &p, int64_t slot, TcChunk &c) {
     if (p.cu) {
@@ -26,12 +26,11 @@ __device__ __forceinline__ bool tc_find_chunk(const SsmArgs &p, int64_t slot, Tc
         const int s = p.cu[n] + kTL * ((int)slot - p.chunk_start[n]);
         c.r0 = s;
         c.nr = min(kTL, p.cu[n + 1] - s);
-        c.seq = n;
     } else {
         const int per = (p.T + kTL - 1) / kTL;
-        c.seq = (int)(slot / per);
+        const int seq = (int)(slot / per);
         const int k = (int)(slot % per);
-        c.r0 = (int64_t)c.seq * p.T + (int64_t)k * kTL;
+        c.r0 = (int64_t)seq * p.T + (int64_t)k * kTL;
         c.nr = min(kTL, p.T - k * kTL);
     }
     return c.nr > 0;

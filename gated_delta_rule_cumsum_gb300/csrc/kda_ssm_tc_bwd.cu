@@ -37,7 +37,7 @@ struct GradUnit {
 };
 struct GradWork {
     int64_t slot;
-    int g, part, first, count, pt, per_group;
+    int g, part, first, count, pt, per_group;  // count >= 1: there are no more parts than units
     TcChunk c;
     __device__ __forceinline__ bool start(const SsmArgs &p) {
         pt = tiles_of(p.P);
@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
         return;
     }
     const int n = w.count;
+    __builtin_assume(n > 0);
     for (int st = 0; st < 2; ++st)  // state rows past Ns are zeros
         for (int e = tid; e < 2 * NK * kPT * 2 / 16; e += kGAll)
             reinterpret_cast<uint4 *>(s.st[st].S)[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -233,12 +234,10 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
             const uint64_t ck = tc::sdesc(tc::smem_addr(s.C), 128, NK * 16);   // K-major
             const uint64_t bk = tc::sdesc(tc::smem_addr(s.B), 128, NK * 16);
             const uint64_t bmn = tc::sdesc(tc::smem_addr(s.B), NK * 16, 128);  // rows = K
-            if (n > 0) {
-                fetch(0);
-                fetch_lo(0);
-            }
+            fetch(0);
+            fetch_lo(0);
             if (n > 1) fetch(1);
-            bool ok = n > 0 && wait_or_die(&s.cb, 0, dead, p.status);
+            bool ok = wait_or_die(&s.cb, 0, dead, p.status);
             tc::tc_fence_after();
             if (ok) {
                 mma_steps(G, ck, 16, bk, 16, tc::idesc_bf16(128, 128, false, false), NK / 16, 0);
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
             if (*dead) {  // what is on its way lands before the block ends
                 for (int it = max(fetched - 2, 0); it < fetched; ++it)
                     tc::mbar_wait(&s.full[it & 1], (it >> 1) & 1, 10000000ull);
-                if (fetched_lo > 0) tc::mbar_wait(&s.lo_full, (fetched_lo - 1) & 1, 10000000ull);
+                tc::mbar_wait(&s.lo_full, (fetched_lo - 1) & 1, 10000000ull);
             }
         }
         __syncwarp();
@@ -308,18 +307,16 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
             load_tile64<AL>(s.st[it & 1].dy, static_cast<const bf16 *>(p.dy) + (w.c.r0 * p.H + u.h) * p.P + col,
                             (int64_t)p.H * p.P, w.c.nr, cols);
         };
-        if (n > 0) {
-            load_wide<AL, NK>(s.C, static_cast<const bf16 *>(p.Cm) + w.c.r0 * p.c_stride + w.g * p.Ns, p.c_stride,
-                              w.c.nr, p.Ns);
-            load_wide<AL, NK>(s.B, static_cast<const bf16 *>(p.Bm) + w.c.r0 * p.b_stride + w.g * p.Ns, p.b_stride,
-                              w.c.nr, p.Ns);
-            load(0);
-            cp_async_wait_all();
-            tc::fence_async_smem();
-            warp_arrive(&s.cb);
-            warp_arrive(&s.rows[0]);
-            wait_or_die(&s.g_done, 0, dead, p.status);
-        }
+        load_wide<AL, NK>(s.C, static_cast<const bf16 *>(p.Cm) + w.c.r0 * p.c_stride + w.g * p.Ns, p.c_stride, w.c.nr,
+                          p.Ns);
+        load_wide<AL, NK>(s.B, static_cast<const bf16 *>(p.Bm) + w.c.r0 * p.b_stride + w.g * p.Ns, p.b_stride, w.c.nr,
+                          p.Ns);
+        load(0);
+        cp_async_wait_all();
+        tc::fence_async_smem();
+        warp_arrive(&s.cb);
+        warp_arrive(&s.rows[0]);
+        wait_or_die(&s.g_done, 0, dead, p.status);
         for (int it = 0; it < n; ++it) {
             const GradUnit u = w.at(p, it);
             auto &st = s.st[it & 1];
@@ -458,11 +455,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_i_kernel(SsmArgs p) {
             }
             bar_sync(1, kGThreads);  // s.rq, s.rs, s.us are free
         }
-        if (n > 0) {
-            store_share<NK>(w.share(p, p.dCh), dC, warp, lane, p.Ns);
-        } else {  // fewer units than parts
-            for (int e = tid; e < kTL * p.Ns; e += kGThreads) w.share(p, p.dCh)[e] = 0.f;
-        }
+        store_share<NK>(w.share(p, p.dCh), dC, warp, lane, p.Ns);
     }
     tmem_close(tm, 512);
 }
@@ -494,6 +487,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
         return;
     }
     const int n = w.count;
+    __builtin_assume(n > 0);
     for (int e = tid; e < 3 * NK * kPT * 2 / 16; e += kGAll)
         reinterpret_cast<uint4 *>(s.E)[e] = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) {
@@ -539,8 +533,8 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             const uint32_t ea = tc::smem_addr(s.E);
             const uint64_t emn = tc::sdesc(ea, kPT * 16, 128), ek = tc::sdesc(ea, 128, kPT * 16);
             constexpr uint64_t emid = NK * kPT * 2 / 16;
-            if (n > 0) fetch(0);
-            bool ok = n > 0 && wait_or_die(&s.cb, 0, dead, p.status);
+            fetch(0);
+            bool ok = wait_or_die(&s.cb, 0, dead, p.status);
             for (int it = 0; it < n; ++it) {
                 const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
                 const uint32_t xa = tc::smem_addr(s.x[it & 1]), ya = tc::smem_addr(s.dy[it & 1]);
@@ -582,7 +576,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
                 // E is free: the products that read it come before those that wait for M
                 if (it + 1 < n && wait_or_die(&s.e_done, ph, dead, p.status)) fetch(it + 1);
             }
-            if (*dead && fetched > 0) tc::mbar_wait(&s.full[(fetched - 1) & 1], ((fetched - 1) >> 1) & 1, 10000000ull);
+            if (*dead) tc::mbar_wait(&s.full[(fetched - 1) & 1], ((fetched - 1) >> 1) & 1, 10000000ull);
         }
         __syncwarp();
     } else {
@@ -600,17 +594,15 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             load_tile64<AL>(s.dy[it & 1], static_cast<const bf16 *>(p.dy) + (w.c.r0 * p.H + u.h) * p.P + col,
                             (int64_t)p.H * p.P, w.c.nr, cols);
         };
-        if (n > 0) {
-            load_wide<AL, NK>(s.C, static_cast<const bf16 *>(p.Cm) + w.c.r0 * p.c_stride + w.g * p.Ns, p.c_stride,
-                              w.c.nr, p.Ns);
-            load_wide<AL, NK>(s.B, static_cast<const bf16 *>(p.Bm) + w.c.r0 * p.b_stride + w.g * p.Ns, p.b_stride,
-                              w.c.nr, p.Ns);
-            load(0);
-            cp_async_wait_all();
-            tc::fence_async_smem();
-            warp_arrive(&s.cb);
-            warp_arrive(&s.rows[0]);
-        }
+        load_wide<AL, NK>(s.C, static_cast<const bf16 *>(p.Cm) + w.c.r0 * p.c_stride + w.g * p.Ns, p.c_stride, w.c.nr,
+                          p.Ns);
+        load_wide<AL, NK>(s.B, static_cast<const bf16 *>(p.Bm) + w.c.r0 * p.b_stride + w.g * p.Ns, p.b_stride, w.c.nr,
+                          p.Ns);
+        load(0);
+        cp_async_wait_all();
+        tc::fence_async_smem();
+        warp_arrive(&s.cb);
+        warp_arrive(&s.rows[0]);
         for (int it = 0; it < n; ++it) {
             const GradUnit u = w.at(p, it);
             const uint32_t ph = it & 1, ph2 = (it >> 1) & 1;
@@ -796,11 +788,7 @@ __global__ void __launch_bounds__(kGAll, 1) ssm_tc_grad_j_kernel(SsmArgs p, int 
             }
             bar_sync(1, kGThreads);
         }
-        if (n > 0) {
-            store_share<NK>(w.share(p, p.dBh), dB, warp, lane, p.Ns);
-        } else {
-            for (int e = tid; e < kTL * p.Ns; e += kGThreads) w.share(p, p.dBh)[e] = 0.f;
-        }
+        store_share<NK>(w.share(p, p.dBh), dB, warp, lane, p.Ns);
     }
     tmem_close(tm, 512);
 }
@@ -955,7 +943,8 @@ cudaError_t grads(const SsmArgs &a, unsigned blocks, cudaStream_t st) {
 
 }  // namespace
 
-// The split of a group's units that takes the fewest rounds of units on 152 SMs.  64 chunks of
+// The split of a group's units, into no more parts than units, that takes the fewest rounds of units
+// on 152 SMs.  64 chunks of
 // one group with 32 units: 2 parts, 387 us for a training pass when this was measured; 1, 4, 5 and
 // 7 parts 558, 409, 462 and 425 us.  Equal stretches over all SMs, across chunks, were slower too: each
 // chunk begins with its B and C and ends with its tile of sums.
