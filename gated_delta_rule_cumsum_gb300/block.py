@@ -427,8 +427,8 @@ class _ConvFunction(torch.autograd.Function):
 
 def short_conv_autograd(x, weight, bias=None, *, initial_state=None, cu_seqlens=None,
                         activation="silu", dev_status=None):
-    """short_conv behind torch.autograd: (y, final state), with gradients to x, weight, bias
-    and the initial state.  `dev_status` is given to the forward and to the backward."""
+    """short_conv behind torch.autograd: (y, final state), with (first-order) gradients to x,
+    weight, bias and the initial state.  `dev_status` is given to the forward and to the backward."""
     return _ConvFunction.apply(x, weight, bias, initial_state, cu_seqlens, activation, dev_status)
 
 
@@ -582,7 +582,7 @@ class _SsmFunction(torch.autograd.Function):
 
 def ssm_scan_autograd(x, dt, A_log, Bm, Cm, *, D=None, dt_bias=None, dt_softplus=True,
                       initial_state=None, cu_seqlens=None, save_for_backward=True, dev_status=None):
-    """ssm_scan behind torch.autograd: (y, ht), with gradients to every floating input.  With
+    """ssm_scan behind torch.autograd: (y, ht), with (first-order) gradients to every floating input.  With
     `save_for_backward` the chunk states are kept from the forward to the backward
     (kda_ssm_workspace_size bytes); False forms them again.  `dev_status` is given to the
     forward and to the backward."""
@@ -670,5 +670,6 @@ class _NormFunction(torch.autograd.Function):
 
 
 def add_rms_norm_autograd(x, weight, *, residual=None, eps=1e-6):
-    """add_rms_norm behind torch.autograd: (y, h), with gradients to x, weight and residual."""
+    """add_rms_norm behind torch.autograd: (y, h), with (first-order) gradients to x, weight and
+    residual."""
     return _NormFunction.apply(x, weight, residual, eps)

@@ -7,6 +7,11 @@
 
 namespace kda {
 
+// The SMs of a GB300.  A constant where a split of the work depends on it: sizes of workspaces follow
+// from some of these splits, and they are asked for without a device.  (Other counts would cost
+// time, not correctness.)
+constexpr int kSms = 152;
+
 // ------------------------------------------------------------ short convolution
 struct ConvArgs {
     const void *x, *state_in;      // [B, T, C] rows x_stride apart; [N, W-1, C]
@@ -133,9 +138,9 @@ cudaError_t launch_ssm_step(const SsmStepArgs &a, kda_dtype dt, cudaStream_t st)
 // kernel that takes part comes to follow(), before it touches what a kernel of the same call
 // wrote (but the chunk table, which is older than the kernel before) and before it returns, so that a
 // kernel's end is also that of all before it.  The first kernel of a call is launched plainly and
-// waits for whatever the stream holds.  Scan, 8192 rows, 32 heads of 64, 128 state rows: training
-// pass of 11 launches 404 us so, 421 with plain launches; with the passes over chunks let in
-// early as well 455, since small blocks crowd on the SMs that are free first.  The CUDA-core
+// waits for whatever the stream holds.  Scan, 8192 rows, 32 heads of 64, 128 state rows: a training
+// pass of 11 launches went from 421 to 404 us with it (388 now, by later steps); with the passes over
+// chunks let in early as well it was 455, since small blocks crowd on the SMs that are free first.  The CUDA-core
 // kernels are launched plainly too (one row of 32 heads, fp32: forward 32 us, 49 let in early).
 __device__ __forceinline__ void follow() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -567,7 +567,7 @@ cudaError_t by_width(int W, F &&f) {
 int strip_for(int64_t rows, int C, int most) {
     const int64_t per_row = (C + kCh - 1) / kCh;
     int strip = most;
-    while (strip > 8 && (rows + strip - 1) / strip * per_row < 152 * 1024) strip /= 2;
+    while (strip > 8 && (rows + strip - 1) / strip * per_row < kSms * 1024) strip /= 2;
     return strip;
 }
 
@@ -653,7 +653,7 @@ cudaError_t launch_conv_step(const ConvStepArgs &a, kda_dtype dt, cudaStream_t s
     const void *ptrs[] = {a.x, a.y, a.state};
     const bool al = rows_aligned(ptrs, 3, (int64_t)(a.C * e), (int64_t)(a.x_stride * e), kCh * e);
     // as many rows per thread as leave 8 blocks for every SM
-    const int64_t cb = channel_blocks(a.C), most = (int64_t)a.N * cb / (152 * 8);
+    const int64_t cb = channel_blocks(a.C), most = (int64_t)a.N * cb / (kSms * 8);
     const int per = most < 1 ? 1 : most > 32 ? 32 : (int)most;
     const int64_t blocks = (a.N + per - 1) / per * cb;
     if (blocks == 0) return cudaSuccess;

@@ -3,15 +3,18 @@
 //
 //     h = x + res,   y = h w / sqrt(mean(h^2) + eps)
 //     8 bits: scale = max |y| / top over a row (or over 128 columns of it; 1 where every
-//     y is 0, NaN where one is), q = round(y / scale), top = 448 (e4m3) or 127 (int8)
+//     y is 0, NaN where one is), q = round(y (1 / scale)), top = 448 (e4m3) or 127 (int8)
 //
 // A row stays in its threads' registers between the sums and the output, so every input
 // is read once and every output written once: bandwidth-bound (2 flops a byte).  The sum
 // h is kept in fp32 for the norm; the stored h is rounded once, beside it.
 //
 // Measured, GB300, bf16: forward 16384 x 2048 43.5 us (268 MB, 6.2 TB/s), 8192 x 4096 to e4m3
-// 48 us (235 MB, 4.9 TB/s); backward 16384 x 2048 52 us (268 MB, 5.2 TB/s).  Rows of 16384
-// columns spill registers in blocks of 1024 threads: 3.8 TB/s forward, 1.7 backward.
+// 48 us (235 MB, 4.9 TB/s); backward 16384 x 2048 52 us (268 MB, 5.2 TB/s).
+// Spills (bytes stored per thread, aligned rows): bf16 forward of 2049 to 4096 columns 8, 28 to 8
+// bits; bf16 backward of 513 to 8192 columns 16; fp32 forward past 4096 columns 84, backward 264; and
+// in blocks of 1024 threads, bf16 past 8192 columns 304 forward and 536 backward, fp32 backward
+// 1064: at 16384 columns 3.7 TB/s forward, 1.7 backward (bf16), 5.7 and 1.5 (fp32).
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -422,7 +425,7 @@ void by_plan(const RowPlan &r, F &&f) {
 // Blocks of either direction: what the GPU's 152 SMs hold at once, at most one per row (the
 // backward leaves one row of partial sums per row that a block works on at a time).
 int64_t row_blocks(int64_t rows, const RowPlan &r, int threads_per_sm) {
-    const int64_t want = 152 * (int64_t)std::max(threads_per_sm / (r.tpr * r.rpb), 1);
+    const int64_t want = kSms * (int64_t)std::max(threads_per_sm / (r.tpr * r.rpb), 1);
     return std::min(want, (rows + r.rpb - 1) / r.rpb);
 }
 int64_t fwd_blocks(int64_t rows, const RowPlan &r) {

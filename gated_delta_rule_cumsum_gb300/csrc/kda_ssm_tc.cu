@@ -7,8 +7,8 @@
 // accumulator: the decay-weighted x of a chunk's state in three (2^-25: the final state is
 // an fp32 output; the smallest part first, since an addition to the full sum may cost it a
 // unit in the last place, however small the addend), the masked gram and the state in front of
-// y in two (2^-17: y is rounded to bf16 at the end).  One part alone would put 2^-9 beside y's
-// own rounding.
+// y in two (2^-17: y is rounded to bf16 at the end).  One part alone would put up to 2^-8,
+// y's own rounding, beside it.
 #include "kda_ssm_tc.cuh"
 
 namespace kda {

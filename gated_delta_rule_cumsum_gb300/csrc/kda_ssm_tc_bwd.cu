@@ -954,7 +954,7 @@ int ssm_tc_parts(int64_t slots, int G, int units) {
     int best = 1;
     int64_t cost = INT64_MAX;
     for (int k = 1; k <= units && k <= 32; ++k) {
-        const int64_t rounds = (items * k + 151) / 152;
+        const int64_t rounds = (items * k + kSms - 1) / kSms;
         const int64_t c = rounds * ((units + k - 1) / k + 1);  // + 1: a CTA's start and end
         if (c < cost) {
             cost = c;

@@ -601,7 +601,8 @@ typedef struct {
  *     y = h w / sqrt(mean(h^2) + eps),
  * and for the 8-bit outputs, per row or group of columns, scale = max|y| / top (1 where
  * every y is 0, at least the smallest normal number elsewhere, and not a number where a y
- * is not) and y rounded to q = y / scale, ties to even.
+ * is not) and q = y (1 / scale), the reciprocal and the product each rounded in fp32, then
+ * rounded to the output's type, ties to even.
  *   x, residual, h  [rows, cols] (h may be NULL: not stored); the norm takes the unrounded sum
  *   w               [cols] fp32
  *   y               [rows, cols]: the shape's type, or one byte per element
