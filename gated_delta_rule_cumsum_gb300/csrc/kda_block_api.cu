@@ -212,6 +212,7 @@ kda_status kda_short_conv_fwd(const void *x, const float *w, const float *bias, 
         return fail(KDA_ERR_INVALID_ARG, "%s: x, w and y must be non-NULL", op);
     if (state_out && state_out == state_in)
         return fail(KDA_ERR_INVALID_ARG, "%s: state_out must not alias state_in", op);
+    if (y && y == x) return fail(KDA_ERR_INVALID_ARG, "%s: y must not alias x", op);
     a.x = x; a.w = w; a.bias = bias; a.state_in = state_in; a.y = y; a.state_out = state_out;
     a.status = dev_status;
     return done(kda::launch_conv_fwd(a, shape->dtype, to_stream(stream)), op);
@@ -238,6 +239,7 @@ kda_status kda_short_conv_bwd(const void *x, const float *w, const float *bias, 
     if ((st = check_workspace(op, workspace, workspace_bytes, kda_short_conv_bwd_workspace_size(shape),
                               16)) != KDA_OK)
         return st;
+    if (dx && (dx == x || dx == dy)) return fail(KDA_ERR_INVALID_ARG, "%s: dx must not alias x or dy", op);
     a.x = x; a.w = w; a.bias = bias; a.state_in = state_in; a.dy = dy; a.dstate_out = dstate_out;
     a.dx = dx; a.dw = dw; a.dbias = dbias; a.dstate_in = dstate_in;
     a.part = static_cast<float *>(workspace);

@@ -460,6 +460,7 @@ size_t kda_chunk_bwd_workspace_size(const kda_shape *shape);
  * (0: contiguous rows); the columns of a row are contiguous and row (b, t) is row
  * b * T + t.  A call takes up to 2^31 - 256 rows (B T).  Outputs are contiguous.  Any
  * alignment of the element type is taken; rows that start on 16-byte boundaries are faster.
+ * Outputs must not overlap inputs, or each other, but where an entry says that they may.
  * State caches.  The step entry points update one row of a cache per batch row, in
  * place: state_indices[n] is row n's slot (NULL: slot n).  A negative entry marks an
  * unused batch row: no state is touched and its output is zero.  An entry past the last

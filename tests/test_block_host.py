@@ -233,3 +233,15 @@ def test_ssm_refuses_row_counts_whose_chunk_count_overflows(kda, T):
                                    None), 2)
     ok = ssm(kda, T=2**31 - 256, H=1, G=1, N=8, P=8)
     assert kda.kda_ssm_workspace_size(ok) > 0
+
+
+def test_conv_refuses_outputs_over_its_inputs(kda):
+    """Strips read the rows before their own while other blocks write theirs."""
+    lib, s = kda.load(), ctypes.byref(conv(kda))
+    x, y, dy, dx, w, ws = (FAKE * k for k in range(1, 7))
+    said(kda, lib.kda_short_conv_fwd(x, w, None, None, None, s, x, None, None, None), 1)
+    assert "alias" in kda.kda_last_error_message()
+    for out in (x, dy):
+        said(kda, lib.kda_short_conv_bwd(x, w, None, None, None, s, dy, None, out, w, None, None, ws, 1 << 30, None,
+                                         None), 1)
+        assert "alias" in kda.kda_last_error_message()
