@@ -1,5 +1,5 @@
 """The recurrent block's operators at sizes where a thread block works on several units, rows or
-groups one after another: rings and barriers come round again, operands are replaced, sums run
+groups one after another: rings and barriers are used again, operands are replaced, sums run
 over a block's units.  Every output against the vectorised fp64 forms of tests/block_reference.py,
 and bit for bit against a second call.
 
