@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         }
         float s[2] = {sum_of(vv), sum_of(ev)};
         team_sum<TS>(s, buf, turn);
-        const float rs = 1.f / sqrtf(s[0] / n + p.eps);
+        // (0 for a team without a row: with eps = 0 its zeros would give the sums NaN)
+        const float rs = live ? 1.f / sqrtf(s[0] / n + p.eps) : 0.f;
         const uint64_t r = both(rs), m = both(-(s[1] / n * rs * rs * rs));
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         for (int e = 0; e < P::N; ++e) ss = fma2(x.v[e], x.v[e], ss);
         float s[1] = {sum_of(ss)};
         team_sum<TS>(s, buf, turn);
-        const float rx = 1.f / sqrtf(s[0] / n + p.eps);
+        const float rx = live ? 1.f / sqrtf(s[0] / n + p.eps) : 0.f;  // (as in the gated norm)
         const uint64_t r = both(rx);
         // h again, and what its norm's gradient needs
 #pragma unroll
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         float two[2] = {sum_of(hh), sum_of(th)};
         fetch(r0 + team + (int64_t)gridDim.x * TPB);  // (asked for ahead of the first sum: 8 us more of 72)
         team_sum<TS>(two, buf, turn);
-        const float rhf = 1.f / sqrtf(two[0] / n + p.eps);
+        const float rhf = live ? 1.f / sqrtf(two[0] / n + p.eps) : 0.f;
         const uint64_t rh = both(rhf), m = both(-(two[1] / n * rhf * rhf * rhf));
         ss = 0;
 #pragma unroll

@@ -1,0 +1,41 @@
+"""The norms around a gated block at the edges of their ranges: eps = 0.  References are the fp64 loops of
+oracle/mixer.py."""
+import pytest
+import torch
+
+from oracle import mixer as om
+
+from .test_gpu_mixer import close, f64, rnd
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 3, 70])
+@pytest.mark.parametrize("cols,group", [(64, 64), (128, 64), (21, 7), (256, 128), (256, 256), (100, 100), (520, 520)])
+def test_norms_without_eps(kda_lib, dtype, rows, cols, group):
+    """Threads of a block that have no row left must not reach the weights' gradients: with eps = 0 the
+    norm of what they hold, zeros, is not a number."""
+    kda, gen = kda_lib, torch.Generator().manual_seed(cols + rows)
+    x, z, res, dy, dh = (rnd(gen, rows, cols, dtype=dtype) for _ in range(5))
+    for w in (rnd(gen, group), rnd(gen, cols)):
+        for first in (False, True):
+            kw = dict(group=group, activation="silu", gate_first=first, eps=0.0)
+            ref = [f64(t) for t in (x, z, w)]
+            close("y", kda.gated_rms_norm(x, z, w, **kw), om.gated_norm(*ref, group, "silu", first, 0.0))
+            d = kda.gated_rms_norm_backward(dy, x, z, w, **kw)
+            want = om.gated_norm_grads(*ref, f64(dy), group, "silu", first, 0.0)
+            for name in want:
+                close(name, d[name], want[name])
+    wa, wb, rs = (rnd(gen, cols) for _ in range(3))
+    for gate in (None, "sigmoid"):
+        kw = dict(gate=z if gate else None, gate_activation=gate, residual_scale=rs, eps=0.0)
+        ref = dict(x=f64(x), res=f64(res), w_post=f64(wa), w_pre=f64(wb), z=f64(kw["gate"]), rs=f64(rs), act=gate, eps=0.0)
+        for name, got, want in zip("yh", kda.sandwich_norm(x, res, wa, wb, **kw), om.sandwich(**ref)):
+            close(name, got, want)
+        d = kda.sandwich_norm_backward(dy, x, res, wa, wb, dresidual_out=dh, **kw)
+        want = om.sandwich_grads(**ref, dy=f64(dy), dh=f64(dh))
+        for name in want:
+            if d[name] is not None:
+                close(name, d[name], want[name])
