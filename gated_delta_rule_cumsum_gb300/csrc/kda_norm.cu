@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) norm_bwd_kernel(NormArgs p, int 
             s[i] = x + y;
         }
         row_sum<2>(s, tpr, red[k & 1]);
-        const float rstd = 1.f / sqrtf(s[0] / (float)p.cols + p.eps);
+        // (0 for threads without a row: with eps = 0 their zeros would give dw NaN)
+        const float rstd = row < p.rows ? 1.f / sqrtf(s[0] / (float)p.cols + p.eps) : 0.f;
         const float m = -s[1] / (float)p.cols * rstd;  // - mean(g xhat)
         const uint64_t rstd2 = pack2(rstd, rstd), m2 = pack2(m, m);
 #pragma unroll
