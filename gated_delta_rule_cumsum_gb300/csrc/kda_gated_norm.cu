@@ -151,21 +151,47 @@ __device__ __forceinline__ float sum_of(uint64_t x) {
     return a + b;
 }
 
-// sigmoid(z), with the fast exponential and division (2^-21 each, next to outputs that are rounded to
-// 2^-9 or sums of a few terms; the exact ones took a third of the kernels' instructions).
-__device__ __forceinline__ float sigmoid_of(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
-__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
+// exp(x) for a gate: of fp32 tensors the exact one (two steps of 2^-23; the division behind it, two more, is the
+// fast one, since the exact one took 4 to 8% of the kernels' time).  bf16 outputs are rounded to 2^-8 and
+// take the fast one, off by its exponent's rounding, (2 + 1.2 |x|) 2^-24: 2^-19 at |x| = 20, 2^-17 at 80.
+template <typename T>
+__device__ __forceinline__ float gate_exp(float x) {
+    if constexpr (sizeof(T) == 2)
+        return __expf(x);
+    else
+        return expf(x);
+}
+// The activated gate.
+template <typename T>
+__device__ __forceinline__ uint64_t gate_of(uint64_t z, int act) {
     float a, b;
     unpack2(z, a, b);
-    return pack2(sigmoid_of(a), sigmoid_of(b));
-}
-// The activated gate and its derivative from z and sigmoid(z).
-__device__ __forceinline__ uint64_t gate_of(uint64_t z, uint64_t s, int act) {
+    const uint64_t s = pack2(__fdividef(1.f, 1.f + gate_exp<T>(-a)), __fdividef(1.f, 1.f + gate_exp<T>(-b)));
     return act == KDA_GATE_SILU ? mul2(z, s) : s;
 }
-__device__ __forceinline__ uint64_t dgate_of(uint64_t z, uint64_t s, int act) {
-    const uint64_t d = fma2(mul2(s, both(-1.f)), s, s);  // s (1 - s)
-    return act == KDA_GATE_SILU ? fma2(z, d, s) : d;
+// m = sigmoid(-|z|), the smaller one of sigmoid(z) and 1 - sigmoid(z), from which the gradients form both: the
+// derivative m (1 - m) keeps its digits where the sigmoid is next to 1, while s (1 - s) of a rounded s is off by
+// 1% at z = 12 and 0 from z = 17 on.
+template <typename T>
+__device__ __forceinline__ uint64_t small_of(uint64_t z) {
+    float a, b;
+    unpack2(z, a, b);
+    const float u = gate_exp<T>(-fabsf(a)), v = gate_exp<T>(-fabsf(b));
+    return pack2(__fdividef(u, 1.f + u), __fdividef(v, 1.f + v));
+}
+__device__ __forceinline__ uint64_t sigmoid_from(uint64_t z, uint64_t m) {  // m or 1 - m
+    float a, b, u, v;
+    unpack2(z, a, b);
+    unpack2(m, u, v);
+    return pack2(fabsf((a < 0.f ? 0.f : 1.f) - u), fabsf((b < 0.f ? 0.f : 1.f) - v));
+}
+__device__ __forceinline__ uint64_t gate_from(uint64_t z, uint64_t m, int act) {
+    const uint64_t s = sigmoid_from(z, m);
+    return act == KDA_GATE_SILU ? mul2(z, s) : s;
+}
+__device__ __forceinline__ uint64_t dgate_from(uint64_t z, uint64_t m, int act) {
+    const uint64_t d = fma2(mul2(m, both(-1.f)), m, m);  // m (1 - m)
+    return act == KDA_GATE_SILU ? fma2(z, d, sigmoid_from(z, m)) : d;
 }
 
 constexpr int kTeamThreads = 256;  // of a block of teams of a warp or less
@@ -222,7 +248,7 @@ __global__ void __launch_bounds__(block_threads(TS), fwd_blocks(TS, VEC * NV, si
         uint64_t ss = 0;
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
-            a.v[e] = gate_of(a.v[e], sigmoid2(a.v[e]), p.act);
+            a.v[e] = gate_of<T>(a.v[e], p.act);
             if (p.first) x.v[e] = mul2(x.v[e], a.v[e]);
             ss = fma2(x.v[e], x.v[e], ss);  // (columns past the group are zeros, whatever the gate)
         }
@@ -308,8 +334,8 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         uint64_t vv = 0, ev = 0;
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
-            sg.v[e] = sigmoid2(z.v[e]);
-            const uint64_t a = gate_of(z.v[e], sg.v[e], p.act);
+            sg.v[e] = small_of<T>(z.v[e]);
+            const uint64_t a = gate_from(z.v[e], sg.v[e], p.act);
             const uint64_t v = p.first ? mul2(x.v[e], a) : x.v[e];  // what is normalised
             uint64_t g = mul2(d.v[e], w.v[e]);                      // dL/d(rms(v))
             if (!p.first) g = mul2(g, a);
@@ -323,7 +349,7 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         const uint64_t r = both(rs), m = both(-(s[1] / n * rs * rs * rs));
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
-            const uint64_t a = gate_of(z.v[e], sg.v[e], p.act), da = dgate_of(z.v[e], sg.v[e], p.act);
+            const uint64_t a = gate_from(z.v[e], sg.v[e], p.act), da = dgate_from(z.v[e], sg.v[e], p.act);
             const uint64_t gw = mul2(d.v[e], w.v[e]), xv = x.v[e];
             if (p.first) {
                 const uint64_t v = mul2(xv, a), dt = fma2(v, m, mul2(r, gw));
@@ -379,7 +405,7 @@ __global__ void __launch_bounds__(block_threads(TS), fwd_blocks(TS, VEC * NV, si
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
             x.v[e] = mul2(mul2(x.v[e], r), w.v[e]);
-            if (GATED) x.v[e] = mul2(x.v[e], gate_of(z.v[e], sigmoid2(z.v[e]), p.act));
+            if (GATED) x.v[e] = mul2(x.v[e], gate_of<T>(z.v[e], p.act));
         }
         weights<TS>(p.rs, t, n, w);
         ss = 0;
@@ -422,7 +448,7 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
     for (int64_t r0 = (int64_t)blockIdx.x * TPB; r0 < p.rows; r0 += (int64_t)gridDim.x * TPB) {
         const bool live = r0 + team < p.rows;
         const int64_t at = (live ? r0 + team : 0) * n;
-        P x, res, z, dy, dh, h, sg, w, f;
+        P x, res, z, dy, dh, h, w, f;
         weights<TS>(p.w_post, t, n, w);
         weights<TS>(p.rs, t, n, f);
         widen(xr, x);
@@ -441,10 +467,7 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
             uint64_t b = mul2(mul2(x.v[e], r), w.v[e]);
-            if (GATED) {
-                sg.v[e] = sigmoid2(z.v[e]);
-                b = mul2(b, gate_of(z.v[e], sg.v[e], p.act));
-            }
+            if (GATED) b = mul2(b, gate_of<T>(z.v[e], p.act));
             h.v[e] = fma2(res.v[e], f.v[e], b);
             hh = fma2(h.v[e], h.v[e], hh);
         }
@@ -467,8 +490,9 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
             res.v[e] = mul2(g, f.v[e]);
             uint64_t ga = g;
             if (GATED) {
-                ga = mul2(g, gate_of(z.v[e], sg.v[e], p.act));
-                z.v[e] = mul2(mul2(mul2(g, w.v[e]), xh), dgate_of(z.v[e], sg.v[e], p.act));
+                const uint64_t sm = small_of<T>(z.v[e]);
+                ga = mul2(g, gate_from(z.v[e], sm, p.act));
+                z.v[e] = mul2(mul2(mul2(g, w.v[e]), xh), dgate_from(z.v[e], sm, p.act));
             }
             dpost.v[e] = fma2(ga, xh, dpost.v[e]);
             dy.v[e] = mul2(ga, w.v[e]);  // dL/d(rms(x))
