@@ -19,7 +19,7 @@
 // column sums it would keep the rounding of far pairs, which cancel.
 #pragma once
 
-#include "kda_block.cuh"
+#include "kda_ssm_tc.cuh"
 
 namespace kda {
 
@@ -34,6 +34,7 @@ struct GdnArgs {
     int32_t *status;
     int64_t q_stride, k_stride, v_stride;
     int B, T, H, HV, K, V, N, l2;
+    int give_up;                   // KDA_GDN_FLAG_TEST_WAIT_TIMEOUT: waits for copies run out at once
     float scale, g_scale;
     int L;                         // chunk length
     int c0, c1;                    // a launch's chunks within every (dense) sequence; c1 == 0: all
@@ -130,6 +131,14 @@ __device__ __forceinline__ bool gdn_find_chunk(const GdnArgs &p, int slot, GdnCh
         c.nr = min(p.L, p.T - k * p.L);
     }
     return c.nr > 0;
+}
+// A wait for copies (see wait_or_die): at its block's end a dead block waits for those it asked for, 10 ms
+// at most, so that they do not land in the shared memory of the block that comes next.
+__device__ __forceinline__ bool copies_or_die(const GdnArgs &p, uint64_t *bar, uint32_t parity, volatile int *dead) {
+    if (!p.give_up) return wait_or_die(bar, parity, dead, p.status);
+    *dead = 1;
+    report(p.status, KDA_DEVICE_TIMEOUT);
+    return false;
 }
 // The chunk slot and value head of a launch's unit; slots * HV fits 31 bits.
 __device__ __forceinline__ void gdn_unit(const GdnArgs &p, int id, int &slot, int &hv) {

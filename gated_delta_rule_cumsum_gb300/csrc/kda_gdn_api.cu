@@ -87,7 +87,7 @@ kda_status check_gdn(const char *op, const kda_gdn_shape *s, const int32_t *cu, 
                     s->V);
     if (s->K > 256 || s->V > 256)
         return fail(KDA_ERR_UNSUPPORTED, "%s: K=%d, V=%d (supported: up to 256)", op, s->K, s->V);
-    if (s->flags & ~(KDA_GDN_FLAG_QK_L2NORM | KDA_GDN_FLAG_NO_SAVE))
+    if (s->flags & ~(KDA_GDN_FLAG_QK_L2NORM | KDA_GDN_FLAG_NO_SAVE | KDA_GDN_FLAG_TEST_WAIT_TIMEOUT))
         return fail(KDA_ERR_UNSUPPORTED, "%s: unknown flag bits 0x%x", op, s->flags);
     if (!std::isfinite(s->scale) || !std::isfinite(s->g_scale))
         return fail(KDA_ERR_INVALID_ARG, "%s: scale and g_scale must be finite", op);
@@ -100,6 +100,7 @@ kda_status check_gdn(const char *op, const kda_gdn_shape *s, const int32_t *cu, 
     a->B = s->B; a->T = s->T; a->H = s->H; a->HV = s->HV; a->K = s->K; a->V = s->V;
     a->N = s->num_seqs;
     a->l2 = (s->flags & KDA_GDN_FLAG_QK_L2NORM) ? 1 : 0;
+    a->give_up = (s->flags & KDA_GDN_FLAG_TEST_WAIT_TIMEOUT) ? 1 : 0;
     a->scale = s->scale > 0.f ? s->scale : 1.f / std::sqrt((float)s->K);
     a->g_scale = s->g_scale;
     a->L = kda::gdn_chunk_len(s->dtype, s->K, s->V);

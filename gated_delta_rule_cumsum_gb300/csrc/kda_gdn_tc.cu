@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
         for (int n = 0; n < nc; ++n) {
             const int at = n % BUFS, turn = n / BUFS & 1;
             const uint8_t *w = s.w[at], *k = s.k[at];
-            bool ok = lane != 0 || wait_or_die(REV ? &s.k_full[at] : &s.w_full[at], turn, dead, p.status);
+            bool ok = lane != 0 || copies_or_die(p, REV ? &s.k_full[at] : &s.w_full[at], turn, dead);
             __syncwarp();
             ahead(n + kAhead);
             bar_sync(1, kScanThreads);  // the state's tile is written
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
                     gdn_mma(D1, desc_k(w) + low, kStepK, right, step, id32, ksteps, 1);
                 }
                 tc::mma_commit(&s.d1);
-                ok = wait_or_die(REV ? &s.w_full[at] : &s.k_full[at], turn, dead, p.status);
+                ok = copies_or_die(p, REV ? &s.w_full[at] : &s.k_full[at], turn, dead);
                 if (wait_or_die(&s.d1, n & 1, dead, p.status)) next(!REV, n + BUFS);
             }
             bar_sync(2, kScanThreads);  // the rows are
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     __syncthreads();
     const int ksteps = (p.K + 15) / 16, cols = (p.V + kSV - 1) / kSV * kSV;
     const uint32_t id_v = tc::idesc_bf16(128, cols, false, true);
-    bool ok = wait_or_die(&s.full, 0, dead, p.status);
+    bool ok = copies_or_die(p, &s.full, 0, dead);
     if (tid == 0 && ok) {
         gdn_mma(G, desc_k(s.q), kStepK, desc_k(s.k), kStepK, tc::idesc_bf16(128, 128, false, false), ksteps, 0);
         gdn_mma(O, desc_k(s.q), kStepK, desc_mn(s.s), kStepMN, id_v, ksteps, 0);
@@ -681,7 +681,9 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     }
     wait_or_die(&s.done, 0, dead, p.status);
     tc::tc_fence_after();
+    int fetches = 1;
     if (tid == 0 && !*dead) {  // U over Q and K
+        ++fetches;
         tc::mbar_arrive_expect_tx(&s.full, 2 * kTile);
         tc::bulk_g2s(s.q, p.ut + unit * 2 * (int64_t)kTile, 2 * kTile, &s.full);
     }
@@ -720,7 +722,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    ok = wait_or_die(&s.full, 1, dead, p.status);
+    ok = copies_or_die(p, &s.full, 1, dead);
     if (tid == 0 && ok) {
         uint64_t u = desc_mn(s.q);
 #pragma unroll 1
@@ -745,7 +747,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
         for (int k = 0; k < 16; ++k) x[k] *= rq;
         if (i < c.nr) store16(o + j0, x, p.V - j0, vec);
     }
-    if (*dead) tc::mbar_wait(&s.full, 1, 10000000ull);
+    if (tid == 0 && *dead) tc::mbar_wait(&s.full, fetches - 1, 10000000ull);  // its copies, if still on their way
     tmem_close(tm, 256);
 }
 

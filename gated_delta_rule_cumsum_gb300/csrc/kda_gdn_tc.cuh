@@ -12,7 +12,6 @@
 #pragma once
 
 #include "kda_gdn.cuh"
-#include "kda_ssm_tc.cuh"
 
 namespace kda {
 namespace {

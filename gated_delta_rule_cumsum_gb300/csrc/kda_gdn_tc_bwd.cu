@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kBaseThreads, 2) gdn_tc_base_kernel(GdnArgs p)
     hand_over();
     const int cols = (p.V + kSV - 1) / kSV * kSV;
     const uint32_t id_t = tc::idesc_bf16(128, cols, true, true);
-    const bool ok = wait_or_die(&s.full, 0, dead, p.status);
+    const bool ok = copies_or_die(p, &s.full, 0, dead);
     if (tid == 0 && ok) {
         gdn_mma(G, desc_k(s.q), kStepK, desc_k(s.k), kStepK, tc::idesc_bf16(128, 128, false, false), (p.K + 15) / 16, 0);
         tc::mma_commit(&s.done);
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kBaseThreads, 2) gdn_tc_base_kernel(GdnArgs p)
     store(R, p.du0 + unit * kGC * kGD);
     all_done();
     store(G, p.b0 + unit * kGC * kGD);
+    if (tid == 0 && *dead) tc::mbar_wait(&s.full, 0, 10000000ull);  // K, if still on its way here
     tmem_close(tm, 256);
 }
 
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
             }
         }
         // ------------------------------------------------ 1
-        bool ok = wait_or_die(&s.full[0], turn, dead, p.status);
+        bool ok = copies_or_die(p, &s.full[0], turn, dead);
         if (tid == 0 && ok) {
             product(T0, desc_mn(A), desc_mn(B), kStepMN, desc_mn(C), desc_mn(D), kStepMN, tc::idesc_bf16(128, cols, true, true),
                     kGC / 16);
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
         // ------------------------------------------------ 2
         cp_async_wait_all();
         hand_over();
-        ok = wait_or_die(&s.full[1], turn, dead, p.status);
+        ok = copies_or_die(p, &s.full[1], turn, dead);
         if (tid == 0 && ok) {
             product(T2, desc_k(C), desc_k(D), kStepK, desc_k(E), desc_k(F), kStepK, id_kk, vsteps);
             product(T3, desc_k(B), 0, kStepK, desc_k(E), desc_k(F), kStepK, id_kk, vsteps);
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
         }
         // ------------------------------------------------ 3
         hand_over();
-        ok = wait_or_die(&s.full[2], turn, dead, p.status);
+        ok = copies_or_die(p, &s.full[2], turn, dead);
         if (tid == 0 && ok) {
             product(T0, desc_k(C), desc_k(D), kStepK, desc_k(A), desc_k(G), kStepK, id_kk, vsteps);
             product(T1, desc_k(B), 0, kStepK, desc_k(A), desc_k(G), kStepK, id_kk, vsteps);
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
             fetch(3, C, p.et + two, 2 * kTile);
             fetch(3, B, k_of(slot, hv), kTile);
         }
-        ok = wait_or_die(&s.full[3], turn, dead, p.status);
+        ok = copies_or_die(p, &s.full[3], turn, dead);
         if (tid == 0 && ok) {
             product(T3, desc_k(E), desc_k(F), kStepK, desc_k(C), desc_k(D), kStepK, id_kk, vsteps);
             tc::mma_commit(&s.done);

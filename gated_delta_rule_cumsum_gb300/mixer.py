@@ -18,7 +18,8 @@ from .block import (_bad, _bytes, _code, _first_order, _indices, _nbytes, _no_gr
                     _on_device, _p, _rows, _s, _same_device, _want, _word)
 
 __all__ = [
-    "KDA_GDN_FLAG_QK_L2NORM", "KDA_GDN_FLAG_NO_SAVE", "KDA_GATE_SIGMOID", "KDA_GATE_SILU",
+    "KDA_GDN_FLAG_QK_L2NORM", "KDA_GDN_FLAG_NO_SAVE", "KDA_GDN_FLAG_TEST_WAIT_TIMEOUT", "KDA_GATE_SIGMOID",
+    "KDA_GATE_SILU",
     "KdaGdnShape", "KdaGatedNormShape", "KdaSandwichShape",
     "kda_gdn_fwd", "kda_gdn_bwd", "kda_gdn_workspace_size", "kda_gdn_bwd_workspace_size", "kda_gdn_step",
     "kda_gated_rmsnorm_fwd", "kda_gated_rmsnorm_bwd", "kda_gated_rmsnorm_bwd_workspace_size",
@@ -29,7 +30,7 @@ __all__ = [
     "sandwich_norm", "sandwich_norm_backward", "sandwich_norm_autograd",
 ]
 
-KDA_GDN_FLAG_QK_L2NORM, KDA_GDN_FLAG_NO_SAVE = 1 << 0, 1 << 1
+KDA_GDN_FLAG_QK_L2NORM, KDA_GDN_FLAG_NO_SAVE, KDA_GDN_FLAG_TEST_WAIT_TIMEOUT = 1 << 0, 1 << 1, 1 << 31
 KDA_GATE_SIGMOID, KDA_GATE_SILU = 0, 1
 
 

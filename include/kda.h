@@ -645,6 +645,11 @@ size_t kda_add_rmsnorm_bwd_workspace_size(const kda_norm_shape *shape);
                                               x / sqrt(sum x^2 + 1e-6)                  */
 #define KDA_GDN_FLAG_NO_SAVE (1u << 1)     /* of a forward: its workspace will not be given
                                               to the backward as `saved`, and may be smaller */
+#define KDA_GDN_FLAG_TEST_WAIT_TIMEOUT (1u << 31)  /* test hook of kda_gdn_fwd and kda_gdn_bwd: the
+                                              kernels' waits for copies give up at once,
+                                              KDA_DEVICE_TIMEOUT is set and they take the path of
+                                              any wait that runs out.  Outputs are undefined;
+                                              never set it in use.                           */
 
 typedef struct {
     int32_t B, T, H, HV, K, V;  /* HV % H == 0; 1 <= K, V <= 256                        */
