@@ -817,28 +817,60 @@ cudaError_t launch_gdn_tc_rscan(const GdnArgs &a, cudaStream_t st) {
                          : run("gdn_tc_rscan", gdn_tc_scan_kernel<true, 1>, scans, kScanThreads, sizeof(ScanSmem<1>), st, a);
 }
 
-// The library's own stream for what runs beside a pass over chunks, and the events that order it: one set
-// per device, made by its first call.  Calls take turns at enqueueing.
-cudaError_t gdn_side(GdnSide **out) {
-    static GdnSide per_dev[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    GdnSide &s = per_dev[dev];
-    if (!s.stream) {
-        int least = 0, greatest = 0;
-        if ((e = cudaDeviceGetStreamPriorityRange(&least, &greatest)) != cudaSuccess) return e;
-        for (cudaEvent_t &ev : s.ev)
-            if (!ev && (e = cudaEventCreateWithFlags(&ev, cudaEventDisableTiming)) != cudaSuccess) return e;
-        if ((e = cudaStreamCreateWithPriority(&s.stream, cudaStreamNonBlocking, least)) != cudaSuccess) return e;
-    }
-    *out = &s;
-    return cudaSuccess;
-}
-std::mutex &gdn_side_lock() {
+// The library's streams for what runs beside a pass over chunks: up to four per device, each made by the
+// first call that needs it.  A call takes one whose work is done, or one that its own stream had last: behind
+// another stream's work, which may stand behind anything, it would wait for that stream.  A taken one
+// belongs to its call alone, so that no lock is held while work is enqueued.
+namespace {
+constexpr int kSides = 4, kDevices = 64;
+GdnSide g_sides[kDevices][kSides];
+std::mutex &sides_lock() {
     static std::mutex mu;
     return mu;
+}
+cudaError_t make_side(GdnSide &s) {
+    int least = 0, greatest = 0;
+    cudaError_t e = cudaDeviceGetStreamPriorityRange(&least, &greatest);
+    for (cudaEvent_t &ev : s.ev)
+        if (e == cudaSuccess && !ev) e = cudaEventCreateWithFlags(&ev, cudaEventDisableTiming);
+    return e == cudaSuccess ? cudaStreamCreateWithPriority(&s.stream, cudaStreamNonBlocking, least) : e;
+}
+}  // namespace
+
+GdnSideHold::GdnSideHold(cudaStream_t st) {
+    int dev = 0;
+    unsigned long long id = 0;
+    if ((error = cudaGetDevice(&dev)) != cudaSuccess || (error = cudaStreamGetId(st, &id)) != cudaSuccess) return;
+    if (dev < 0 || dev >= kDevices) return;
+    // (asking for an event would end another thread's capture that forbids such calls)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if ((error = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess) return;
+    {
+        std::lock_guard<std::mutex> lock(sides_lock());
+        GdnSide *idle = nullptr;
+        for (GdnSide &s : g_sides[dev]) {
+            if (s.taken) continue;
+            if (s.last && s.of == id) {
+                idle = &s;
+                break;
+            }
+            if (!idle && (!s.last || cudaEventQuery(s.last) == cudaSuccess)) idle = &s;
+        }
+        cudaGetLastError();  // (a query's "not ready")
+        if (idle && !idle->stream) error = make_side(*idle);
+        if (idle && error == cudaSuccess) {
+            idle->taken = true;
+            idle->of = id;
+            side = idle;
+        }
+    }
+    const cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (error == cudaSuccess) error = e;
+}
+GdnSideHold::~GdnSideHold() {
+    if (!side) return;
+    std::lock_guard<std::mutex> lock(sides_lock());
+    side->taken = false;
 }
 
 // Where to cut a dense sequence's chunks in two for pipelined launches, from the front; 0: not at all.  While a
@@ -869,7 +901,10 @@ cudaError_t launch_gdn_tc_fwd(const GdnArgs &a, cudaStream_t st) {
     cudaError_t e = prepare_kernels();
     if (e != cudaSuccess) return e;
     const int m = gdn_cut(a, kPrepNs, kRoundNs, 512, st);
-    if (m == 0) {
+    std::optional<GdnSideHold> hold;
+    if (m > 0 && (e = hold.emplace(st).error) != cudaSuccess) return e;
+    GdnSide *const s = hold ? hold->side : nullptr;
+    if (!s) {
         const int64_t units = a.slots * a.HV;
         if ((e = launch_prep(a, units, st)) != cudaSuccess) return e;
         if ((e = launch_scan(a, st)) != cudaSuccess) return e;
@@ -877,9 +912,6 @@ cudaError_t launch_gdn_tc_fwd(const GdnArgs &a, cudaStream_t st) {
     }
     // chunks [0, m) and [m, nc): the second part's matrices beside the first's pass, the first's outputs beside
     // the second's
-    std::lock_guard<std::mutex> lock(gdn_side_lock());
-    GdnSide *s = nullptr;
-    if ((e = gdn_side(&s)) != cudaSuccess) return e;
     GdnArgs x = a, y = a;
     x.c0 = 0;
     x.c1 = y.c0 = m;

@@ -11,6 +11,8 @@
 // (2^-9) goes only into products behind a bf16 output, next to whose own rounding it stands.
 #pragma once
 
+#include <optional>
+
 #include "kda_gdn.cuh"
 
 namespace kda {
@@ -144,17 +146,31 @@ __device__ __forceinline__ int64_t wide_at(int t, int g, int r) { return ((int64
 }  // namespace
 
 cudaError_t launch_gdn_tc_fwd(const GdnArgs &a, cudaStream_t st);
+// One of the library's own streams, for what runs beside a pass over chunks, and the events that order it.
 struct GdnSide {
     cudaStream_t stream = nullptr;
     cudaEvent_t ev[4] = {};
+    cudaEvent_t last = nullptr;    // of ev: behind all that the stream holds
+    unsigned long long of = 0;     // the caller's stream that had it last
+    bool taken = false;            // by a call that is enqueueing
     // `st` after all that the side stream holds
     cudaError_t join(int i, cudaStream_t st) {
         const cudaError_t e = cudaEventRecord(ev[i], stream);
+        if (e == cudaSuccess) last = ev[i];
         return e != cudaSuccess ? e : cudaStreamWaitEvent(st, ev[i], 0);
     }
 };
-cudaError_t gdn_side(GdnSide **out);
-std::mutex &gdn_side_lock();
+// A call's hold on a side stream that holds no other stream's work, for as long as the call enqueues; side is
+// null where there is none, and the call then runs in one part.
+class GdnSideHold {
+  public:
+    explicit GdnSideHold(cudaStream_t st);
+    ~GdnSideHold();
+    GdnSideHold(const GdnSideHold &) = delete;
+    GdnSideHold &operator=(const GdnSideHold &) = delete;
+    GdnSide *side = nullptr;
+    cudaError_t error = cudaSuccess;
+};
 int gdn_cut(const GdnArgs &a, double unit_ns, double round_ns, int64_t least, cudaStream_t st);
 // Measured: the whole card's time per unit of the prep and of the gradients, and a pass's round.
 constexpr double kPrepNs = 85, kGradNs = 205, kRoundNs = 2200;

@@ -661,16 +661,16 @@ cudaError_t launch_gdn_tc_bwd(const GdnArgs &a, cudaStream_t st) {
                    kGradThreads, sizeof(GradSmem), on, x, (int)(a.HV == a.H), wide);
     };
     const int m = gdn_cut(a, kGradNs, kRoundNs, 256, st);
-    if (m == 0) {
+    std::optional<GdnSideHold> hold;
+    if (m > 0 && (e = hold.emplace(st).error) != cudaSuccess) return e;
+    GdnSide *const s = hold ? hold->side : nullptr;
+    if (!s) {
         const int64_t units = a.slots * a.HV;
         if ((e = base(a, units, st)) != cudaSuccess) return e;
         if ((e = launch_gdn_tc_rscan(a, st)) != cudaSuccess) return e;
         return grad(a, units, kSms, st);
     }
     // chunks [m, nc) first, then [0, m): the second's base products and the first's gradients beside the passes
-    std::lock_guard<std::mutex> lock(gdn_side_lock());
-    GdnSide *s = nullptr;
-    if ((e = gdn_side(&s)) != cudaSuccess) return e;
     GdnArgs x = a, y = a;
     x.c0 = m;
     x.c1 = (a.T + a.L - 1) / a.L;

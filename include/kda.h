@@ -41,9 +41,9 @@
  * Memory.  Every tensor pointer is a DEVICE pointer owned by the caller, on
  * the current CUDA device.  The library allocates no memory and keeps no
  * global state beyond a per-process cache of device attributes and, once a
- * pipelined call has run on a device, a stream and events there: one stream and
- * two events for kda_chunk_fwd (KDA_FLAG_SERIAL), one stream of the lowest
- * priority and four events for kda_gdn_fwd and kda_gdn_bwd.  All work is
+ * pipelined call has run on a device, streams and events there: one stream and
+ * two events for kda_chunk_fwd (KDA_FLAG_SERIAL), up to four streams of the lowest
+ * priority with four events each for kda_gdn_fwd and kda_gdn_bwd.  All work is
  * enqueued on `stream` (NULL = the legacy default stream), or ordered by events
  * between what `stream` holds and what comes on it next; calls return without
  * synchronising, except kda_read_device_status.
@@ -665,8 +665,8 @@ typedef struct {
 /*
  * kda_gdn_fwd -- the chunked forward.  Dense calls of long sequences and few heads, outside a
  * stream capture, run in two parts that overlap on a stream of the library's own, which waits
- * for `stream` and is waited for on it; calls made at the same time then take turns at
- * enqueueing.
+ * for `stream` and is waited for on it.  A call never waits for another stream's: where every
+ * stream of the library's still has some of another's work, it runs in one part, with the same bits.
  *   q, k       [B, T, H, K];  v [B, T, HV, V];  beta [B, T, HV]
  *   g          [B, T, HV] fp32
  *   h0, ht     [num_seqs, HV, K, V] fp32 or NULL, as for kda_chunk_fwd; ht may alias h0
