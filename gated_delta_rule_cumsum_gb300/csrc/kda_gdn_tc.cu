@@ -639,7 +639,8 @@ constexpr int kOutThreads = 256;
 struct OutSmem {
     uint8_t q[kTile], k[kTile], s[kTile];  // Q, then U's high part; K, then U's low part; the state
     float row[kGdnRowArrays * kGC];
-    uint64_t full, done;
+    // a barrier for each use: a thread that has not seen a phase end yet would wait for the one two later
+    uint64_t full[2], done[2];
     uint32_t slot_addr;
     int dead;
 };
@@ -655,13 +656,15 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     GdnChunk c;
     if (!gdn_find_chunk(p, slot, c)) return;
     if (tid == 0) {
-        tc::mbar_init(&s.full, 1);
-        tc::mbar_init(&s.done, 1);
+        for (int k = 0; k < 2; ++k) {
+            tc::mbar_init(&s.full[k], 1);
+            tc::mbar_init(&s.done[k], 1);
+        }
         tc::mbar_fence_init();
         s.dead = 0;
-        tc::mbar_arrive_expect_tx(&s.full, 2 * kTile);
-        tc::bulk_g2s(s.k, p.kt + ((int64_t)slot * p.H + h) * kTile, kTile, &s.full);
-        tc::bulk_g2s(s.s, p.st + unit * (p.mt ? 2 : 1) * (int64_t)kTile, kTile, &s.full);
+        tc::mbar_arrive_expect_tx(&s.full[0], 2 * kTile);
+        tc::bulk_g2s(s.k, p.kt + ((int64_t)slot * p.H + h) * kTile, kTile, &s.full[0]);
+        tc::bulk_g2s(s.s, p.st + unit * (p.mt ? 2 : 1) * (int64_t)kTile, kTile, &s.full[0]);
     }
     const uint32_t tm = tmem_open(&s.slot_addr, 256), G = tm, O = tm + 128;
     volatile int *dead = &s.dead;
@@ -673,19 +676,19 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     __syncthreads();
     const int ksteps = (p.K + 15) / 16, cols = (p.V + kSV - 1) / kSV * kSV;
     const uint32_t id_v = tc::idesc_bf16(128, cols, false, true);
-    bool ok = copies_or_die(p, &s.full, 0, dead);
+    bool ok = copies_or_die(p, &s.full[0], 0, dead);
     if (tid == 0 && ok) {
         gdn_mma(G, desc_k(s.q), kStepK, desc_k(s.k), kStepK, tc::idesc_bf16(128, 128, false, false), ksteps, 0);
         gdn_mma(O, desc_k(s.q), kStepK, desc_mn(s.s), kStepMN, id_v, ksteps, 0);
-        tc::mma_commit(&s.done);
+        tc::mma_commit(&s.done[0]);
     }
-    wait_or_die(&s.done, 0, dead, p.status);
+    wait_or_die(&s.done[0], 0, dead, p.status);
     tc::tc_fence_after();
     int fetches = 1;
     if (tid == 0 && !*dead) {  // U over Q and K
         ++fetches;
-        tc::mbar_arrive_expect_tx(&s.full, 2 * kTile);
-        tc::bulk_g2s(s.q, p.ut + unit * 2 * (int64_t)kTile, 2 * kTile, &s.full);
+        tc::mbar_arrive_expect_tx(&s.full[1], 2 * kTile);
+        tc::bulk_g2s(s.q, p.ut + unit * 2 * (int64_t)kTile, 2 * kTile, &s.full[1]);
     }
     const GdnRows rd(s.row, kGC);
     const float ai = rd.a[i], li = rd.lo[i], rq = rd.rq[i], ci = rd.c[i];
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    ok = copies_or_die(p, &s.full, 1, dead);
+    ok = copies_or_die(p, &s.full[1], 0, dead);
     if (tid == 0 && ok) {
         uint64_t u = desc_mn(s.q);
 #pragma unroll 1
@@ -732,9 +735,9 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
             mma_bf16_ts(O, G + 8 * k, u, id_v, 1);
             u += kStepMN;
         }
-        tc::mma_commit(&s.done);
+        tc::mma_commit(&s.done[1]);
     }
-    wait_or_die(&s.done, 1, dead, p.status);
+    wait_or_die(&s.done[1], 0, dead, p.status);
     tc::tc_fence_after();
     bf16 *o = static_cast<bf16 *>(p.o) + ((c.r0 + i) * p.HV + hv) * (int64_t)p.V;
 #pragma unroll 1
@@ -747,7 +750,8 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
         for (int k = 0; k < 16; ++k) x[k] *= rq;
         if (i < c.nr) store16(o + j0, x, p.V - j0, vec);
     }
-    if (tid == 0 && *dead) tc::mbar_wait(&s.full, fetches - 1, 10000000ull);  // its copies, if still on their way
+    if (tid == 0 && *dead)  // its copies, if still on their way
+        for (int k = 0; k < fetches; ++k) tc::mbar_wait(&s.full[k], 0, 10000000ull);
     tmem_close(tm, 256);
 }
 

@@ -157,7 +157,9 @@ constexpr int kGradThreads = 512;
 struct GradSmem {
     uint8_t t[7][kTile];
     float red[4][kGC], small[32];
-    uint64_t full[4], done;
+    // (done's next phase must not end before every thread has seen this one end: a thread that had not would wait
+    // for the one after.  Two products follow each other without a barrier between, so the second has its own)
+    uint64_t full[4], done, done_e;
     uint32_t slot_addr;
     int dead;
 };
@@ -215,6 +217,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
     if (tid == 0) {
         for (int k = 0; k < 4; ++k) tc::mbar_init(&s.full[k], 1);
         tc::mbar_init(&s.done, 1);
+        tc::mbar_init(&s.done_e, 1);
         tc::mbar_fence_init();
         s.dead = 0;
         const int64_t two = two_of(slot, hv);
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
         ok = copies_or_die(p, &s.full[3], turn, dead);
         if (tid == 0 && ok) {
             product(T3, desc_k(E), desc_k(F), kStepK, desc_k(C), desc_k(D), kStepK, id_kk, vsteps);
-            tc::mma_commit(&s.done);
+            tc::mma_commit(&s.done_e);
         }
         float es = 0.f;  // <S, E>, a share
         for (int k = 0; k < 32; k += 8)
@@ -448,7 +451,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
 #pragma unroll
                 for (int e = 0; e < 8; ++e) es = fmaf(a[e] + b[e], x[e] + y[e], es);
             }
-        all_done();
+        wait_or_die(&s.done_e, turn, dead, p.status);
+        tc::tc_fence_after();
         // Q over U; X and Y over the state
         load_tile_rows<AL, kGradThreads>(E, qrows, p.q_stride, c.nr, p.K, tid);
         __syncthreads();

@@ -89,3 +89,23 @@ def test_two_host_threads(kda_lib):
         for t in threads:
             t.join()
         assert not errors, errors
+
+
+def test_no_wait_runs_out_beside_other_calls(kda_lib):
+    """Blocks of several kernels on an SM hold each other's threads up: a thread that comes late to a wait
+    must still find its phase."""
+    gen = torch.Generator().manual_seed(9)
+    calls, streams = [call_of(gen) for _ in range(3)], [torch.cuda.Stream() for _ in range(3)]
+    status = [kda_lib.new_status() for _ in calls]
+    want = [both_ways(kda_lib, *c, qk_l2norm=True) for c in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [[] for _ in calls]
+        for _ in range(4):
+            for n, (s, c) in enumerate(zip(streams, calls)):
+                with torch.cuda.stream(s):
+                    got[n].append(both_ways(kda_lib, *c, qk_l2norm=True, dev_status=status[n]))
+        torch.cuda.synchronize()
+        assert all(kda_lib.kda_read_device_status(w) == (kda_lib.KDA_OK, 0) for w in status)
+        for n in range(3):
+            assert all(same(g, want[n]) for g in got[n])
