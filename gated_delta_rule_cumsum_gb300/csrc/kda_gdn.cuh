@@ -48,8 +48,7 @@ struct GdnArgs {
     // of 4] each); per 32 value columns, the state at the chunk's start ([K][32]) and U ([L][32])
     float *mats, *wk, *states, *us;
     // tensor-core path, per unit (kda_gdn_tc.cuh; a tile is 32 KB, two parts two tiles): M (null: not
-    // kept, and then the states with their high parts only), W, the state at the chunk's
-    // start, U; U0 in fp32; and per (slot, head) K
+    // kept), W, the state at the chunk's start, U; U0 in fp32; and per (slot, head) K
     uint8_t *mt, *wt, *st, *ut, *kt;
     float *u0;
     float *carry;                  // [N][HV][K][V]: the state between two launches of a pass

@@ -32,7 +32,7 @@ GdnWs gdn_ws(const kda_gdn_shape *s) {
     if (kda::gdn_tc_supported(s->dtype, s->K, s->V)) {
         const size_t tile = kda::kGdnTile;
         w.states = w.wk = w.mats;
-        w.us = w.states + units * (save ? 2 : 1) * tile;
+        w.us = w.states + units * 2 * tile;
         w.mt = w.us + units * 2 * tile;
         w.wt = w.mt + (save ? units * 2 * tile : 0);
         w.u0 = w.wt + units * 2 * tile;

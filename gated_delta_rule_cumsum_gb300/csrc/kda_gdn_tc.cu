@@ -509,8 +509,6 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
     for (int k = 0; k < 16; ++k) st[k] = from && k < have ? from[user + k] : 0.f;
     uint8_t *keep = REV ? p.et : p.st;           // the states' tiles
     uint8_t *out = REV ? p.dut : p.ut;           // the rows' tiles
-    const bool lows = REV || p.mt != nullptr;    // the states with their low parts
-    const int64_t hop = lows ? 2 * (int64_t)kTile : (int64_t)kTile;
     const float *base = REV ? p.du0 : p.u0;
     // 16 columns of row i as two parts, into the right operand's tile; and into a unit's tiles, behind
     // the products that wait for the first
@@ -530,11 +528,12 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
             *reinterpret_cast<uint4 *>(s.right + tc::tile_off(i, 32 + hf * 16 + 8 * k, 64)) = u.lo[k];
         }
     };
-    auto store = [&](const Parts &u, uint8_t *to, bool low) {
+    auto store = [&](const Parts &u, uint8_t *tiles, int64_t unit) {
+        uint8_t *to = tiles + unit * 2 * (int64_t)kTile;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             *reinterpret_cast<uint4 *>(to + gtile(i, c0 + 8 * k)) = u.hi[k];
-            if (low) *reinterpret_cast<uint4 *>(to + kTile + gtile(i, c0 + 8 * k)) = u.lo[k];
+            *reinterpret_cast<uint4 *>(to + kTile + gtile(i, c0 + 8 * k)) = u.lo[k];
         }
     };
     auto ld_sum = [&](uint32_t d, float (&x)[16]) {  // the two parts' products
@@ -571,7 +570,7 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
         put(u);
         hand_over(1);
         fetch_rows(0);
-        store(u, keep + (slot_of(0) * p.HV + hv) * hop, lows);
+        store(u, keep, slot_of(0) * p.HV + hv);
     }
     for (int n = 0; n < nc; ++n) {
         const int64_t unit = slot_of(n) * p.HV + hv;
@@ -605,7 +604,7 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
         }
         if (!REV) u = parts(x);
         const Parts made = u;
-        if (REV || BUFS == 1) store(made, out + unit * 2 * (int64_t)kTile, true);
+        if (REV || BUFS == 1) store(made, out, unit);
         if (n + 1 < nc) fetch_rows(n + 1);
         wait_or_die(&s.d2, n & 1, dead, p.status);
         tc::tc_fence_after();
@@ -616,11 +615,11 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
             u = parts(st);
             put(u);
             hand_over(1);
-            store(u, keep + (slot_of(n + 1) * p.HV + hv) * hop, lows);
+            store(u, keep, slot_of(n + 1) * p.HV + hv);
         }
         // U's tiles: the hand-over's fence would wait for these stores (139 -> 132 us; the reverse pass, whose
         // registers are full, took 163 so, 145 with the stores ahead)
-        if (!REV && BUFS > 1) store(made, out + unit * 2 * (int64_t)kTile, true);
+        if (!REV && BUFS > 1) store(made, out, unit);
     }
     float *to = REV ? (lo > 0 ? p.dcarry : p.dh0) : (hi < all ? p.carry : p.ht);
 #pragma unroll
@@ -632,15 +631,17 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
 // ------------------------------------------------------------------ outputs
 // O = diag(rq) (diag(c) Q S + P U) for a chunk, one block each, two on an SM.  P and U are two bf16
 // parts: where keys are alike, U's rows nearly cancel in the sum (one part each left o off by 3% of
-// its largest value for keys that are all but the same).  The state enters with one part.  P is a
-// left operand in tensor memory, over the gram it is made of, and its products are added to the
-// state's.  8192 rows of 16 heads: 46 us for 200 MB, 4.3 TB/s; 4 x 4096 rows of 32 heads 132 us.
+// its largest value for keys that are all but the same); so is the state (one part left o off by half of what
+// its own rounding does, and the kernel at 132 of its 155 us).  P is a left operand in tensor memory, over the gram it is
+// made of, and its products are added to the state's.  Of the seven tiles three have room at a time: each is fetched
+// as soon as the product with the one before it is through.  8192 rows of 16 heads: 54 us for 230 MB, 4.3 TB/s; 4 x 4096
+// rows of 32 heads 155 us.
 constexpr int kOutThreads = 256;
 struct OutSmem {
-    uint8_t q[kTile], k[kTile], s[kTile];  // Q, then U's high part; K, then U's low part; the state
+    uint8_t q[kTile], k[kTile], s[kTile];  // Q, then U's low part; K, then the state's low part; its high part, then U's
     float row[kGdnRowArrays * kGC];
     // a barrier for each use: a thread that has not seen a phase end yet would wait for the one two later
-    uint64_t full[2], done[2];
+    uint64_t full[3], done[3];
     uint32_t slot_addr;
     int dead;
 };
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     GdnChunk c;
     if (!gdn_find_chunk(p, slot, c)) return;
     if (tid == 0) {
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 3; ++k) {
             tc::mbar_init(&s.full[k], 1);
             tc::mbar_init(&s.done[k], 1);
         }
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
         s.dead = 0;
         tc::mbar_arrive_expect_tx(&s.full[0], 2 * kTile);
         tc::bulk_g2s(s.k, p.kt + ((int64_t)slot * p.H + h) * kTile, kTile, &s.full[0]);
-        tc::bulk_g2s(s.s, p.st + unit * (p.mt ? 2 : 1) * (int64_t)kTile, kTile, &s.full[0]);
+        tc::bulk_g2s(s.s, p.st + unit * 2 * (int64_t)kTile, kTile, &s.full[0]);
     }
     const uint32_t tm = tmem_open(&s.slot_addr, 256), G = tm, O = tm + 128;
     volatile int *dead = &s.dead;
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     __syncthreads();
     const int ksteps = (p.K + 15) / 16, cols = (p.V + kSV - 1) / kSV * kSV;
     const uint32_t id_v = tc::idesc_bf16(128, cols, false, true);
-    bool ok = copies_or_die(p, &s.full[0], 0, dead);
+    const bool ok = copies_or_die(p, &s.full[0], 0, dead);
     if (tid == 0 && ok) {
         gdn_mma(G, desc_k(s.q), kStepK, desc_k(s.k), kStepK, tc::idesc_bf16(128, 128, false, false), ksteps, 0);
         gdn_mma(O, desc_k(s.q), kStepK, desc_mn(s.s), kStepMN, id_v, ksteps, 0);
@@ -685,10 +686,11 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     wait_or_die(&s.done[0], 0, dead, p.status);
     tc::tc_fence_after();
     int fetches = 1;
-    if (tid == 0 && !*dead) {  // U over Q and K
+    if (tid == 0 && !*dead) {
         ++fetches;
         tc::mbar_arrive_expect_tx(&s.full[1], 2 * kTile);
-        tc::bulk_g2s(s.q, p.ut + unit * 2 * (int64_t)kTile, 2 * kTile, &s.full[1]);
+        tc::bulk_g2s(s.k, p.st + unit * 2 * (int64_t)kTile + kTile, kTile, &s.full[1]);
+        tc::bulk_g2s(s.s, p.ut + unit * 2 * (int64_t)kTile, kTile, &s.full[1]);
     }
     const GdnRows rd(s.row, kGC);
     const float ai = rd.a[i], li = rd.lo[i], rq = rd.rq[i], ci = rd.c[i];
@@ -701,6 +703,17 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
         decays16(rd, i, quad, j0 / 16, ai, li, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) split2(v[2 * k] * w[2 * k], v[2 * k + 1] * w[2 * k + 1], hi[J * 8 + k], lo[J * 8 + k]);
+        if (J == 2 && tid == 0 && copies_or_die(p, &s.full[1], 0, dead)) {
+            gdn_mma(O, desc_k(s.q), kStepK, desc_mn(s.k), kStepMN, id_v, ksteps, 1);
+            tc::mma_commit(&s.done[1]);
+        }
+    }
+    wait_or_die(&s.done[1], 0, dead, p.status);
+    tc::tc_fence_after();
+    if (tid == 0 && !*dead) {
+        ++fetches;
+        tc::mbar_arrive_expect_tx(&s.full[2], kTile);
+        tc::bulk_g2s(s.q, p.ut + unit * 2 * (int64_t)kTile + kTile, kTile, &s.full[2]);
     }
 #pragma unroll 1
     for (int J = 0; J < 8; ++J) {
@@ -725,19 +738,19 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    ok = copies_or_die(p, &s.full[1], 0, dead);
-    if (tid == 0 && ok) {
-        uint64_t u = desc_mn(s.q);
+    if (tid == 0 && !*dead) {
+        const uint64_t u = desc_mn(s.s), ul = desc_mn(s.q);
 #pragma unroll 1
-        for (int k = 0; k < kGC / 16; ++k) {
-            mma_bf16_ts(O, G + 64 + 8 * k, u, id_v, 1);
-            mma_bf16_ts(O, G + 8 * k, u + kTile / 16, id_v, 1);
-            mma_bf16_ts(O, G + 8 * k, u, id_v, 1);
-            u += kStepMN;
+        for (int k = 0; k < kGC / 16; ++k) mma_bf16_ts(O, G + 64 + 8 * k, u + k * kStepMN, id_v, 1);
+#pragma unroll 1
+        for (int k = 0; k < kGC / 16; ++k) mma_bf16_ts(O, G + 8 * k, u + k * kStepMN, id_v, 1);
+        if (copies_or_die(p, &s.full[2], 0, dead)) {
+#pragma unroll 1
+            for (int k = 0; k < kGC / 16; ++k) mma_bf16_ts(O, G + 8 * k, ul + k * kStepMN, id_v, 1);
+            tc::mma_commit(&s.done[2]);
         }
-        tc::mma_commit(&s.done[1]);
     }
-    wait_or_die(&s.done[1], 0, dead, p.status);
+    wait_or_die(&s.done[2], 0, dead, p.status);
     tc::tc_fence_after();
     bf16 *o = static_cast<bf16 *>(p.o) + ((c.r0 + i) * p.HV + hv) * (int64_t)p.V;
 #pragma unroll 1
