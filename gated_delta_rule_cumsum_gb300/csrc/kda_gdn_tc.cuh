@@ -6,9 +6,8 @@
 // whole groups of 16 contracted columns and of 32 value columns are worked on.
 //
 // Precision.  The inputs enter the products as they are (the norm is a factor of the row).  What the
-// kernels make themselves and what reaches an fp32 output (the states, dg, dh0) is split into two bf16
-// parts, and two or three products add up in one accumulator: 2^-17 of each factor.  One part alone
-// (2^-9) goes only into products behind a bf16 output, next to whose own rounding it stands.
+// kernels make themselves is split into two bf16 parts, and two or three products add up in one
+// accumulator: 2^-17 of each factor, so that the bf16 outputs are the exact ones rounded once.
 #pragma once
 
 #include <optional>

@@ -145,14 +145,15 @@ __global__ void __launch_bounds__(kBaseThreads, 2) gdn_tc_base_kernel(GdnArgs p)
 //   1  Z = M^T dU (2, 2);  K K^T
 //   2  Z U^T (2, 2);  dO U^T (1, 2);  Q K^T        -> X, Y and the pairs' sums
 //   3  Z S^T (2, 2);  dO S^T (1, 2);  U E^T (2, 2)  -> the rows' sums
-//   4  X K, X^T Q, (Y + Y^T) K (1, 1), added to the rows' shares of step 3
+//   4  X K, X^T Q, (Y + Y^T) K (2, 1), added to the rows' shares of step 3
 // X and Y carry both rows' norm factors, so that what step 4 leaves is dq and dk but for the norm's
 // projection.
 // Each block takes every n-th unit; the next unit's tiles are fetched as soon as this one's leave room
 // (224 KB are a quarter of a unit's time), which moves the tiles' parts around: see the loop's end.
-// 8192 rows of 16 heads: 208 us, 31 us a unit, of which its products take 6.  One unit an SM is a chain of
+// 8192 rows of 16 heads: 225 us, 33 us a unit, of which its products take 7.  One unit an SM is a chain of
 // four rounds of products and what the threads do between them; HBM is 34% busy, and no shared memory is left
-// for a second unit.
+// for a second unit.  X and Y with one part each (208 us) left dq and dk off by 2.5e-3 from the rounded ones; their
+// low parts by bulk copies, which want a fence between the threads' writes and the copy, 240 us.
 constexpr int kGradThreads = 512;
 struct GradSmem {
     uint8_t t[7][kTile];
@@ -354,6 +355,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
             fetch(2, G, p.st + two + kTile, kTile);
         }
         float pairs = 0.f;  // thread t < 128: the sum over the pairs that row t's decay lies between
+        // X's and Y's low parts wait in memory (P^T dO's place), for lack of any other room: eight columns of X,
+        // then of Y, at a time; a thread reads what it wrote
+        uint4 *const lows = reinterpret_cast<uint4 *>(p.du0 + unit * kGC * kGD) + tid;
         {
             uint32_t xs[16] = {}, ys[16] = {};
             float f[32];  // the pairs' shares, then their sums from the thread's first column on
@@ -381,11 +385,15 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
                             g[k] = -bi * a;
                             f[J * 16 + q * 8 + k] = fmaf(hh[k], qk[k], g[k] * kk[k]);
                         }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            xs[J * 8 + q * 4 + k] = pack_bf16(hh[2 * k], hh[2 * k + 1]);
-                            ys[J * 8 + q * 4 + k] = pack_bf16(g[2 * k], g[2 * k + 1]);
-                        }
+                        uint4 a, b;
+                        split8(hh, a, b);
+                        lows[(J * 2 + q) * kGradThreads] = b;
+                        xs[J * 8 + q * 4] = a.x; xs[J * 8 + q * 4 + 1] = a.y;
+                        xs[J * 8 + q * 4 + 2] = a.z; xs[J * 8 + q * 4 + 3] = a.w;
+                        split8(g, a, b);
+                        lows[(4 + J * 2 + q) * kGradThreads] = b;
+                        ys[J * 8 + q * 4] = a.x; ys[J * 8 + q * 4 + 1] = a.y;
+                        ys[J * 8 + q * 4 + 2] = a.z; ys[J * 8 + q * 4 + 3] = a.w;
                     }
                 }
                 beta_sum -= ag;
@@ -453,14 +461,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
             }
         wait_or_die(&s.done_e, turn, dead, p.status);
         tc::tc_fence_after();
-        // Q over U; X and Y over the state
+        // Q over U; X and Y over the state, their low parts over E
         load_tile_rows<AL, kGradThreads>(E, qrows, p.q_stride, c.nr, p.K, tid);
+        uint4 low[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            low[k] = c0 <= quad * 32 + 31 ? lows[k * kGradThreads] : make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        if (tid == 0 && more && !*dead) {  // the next unit's dU and K; M below
+        if (tid == 0 && more && !*dead) {  // the next unit's K; dU and M below
             ++armed[0];
             tc::mbar_arrive_expect_tx(&s.full[0], 5 * kTile);
-            fetch(0, C, p.dut + two_of(next_slot, next_hv), 2 * kTile);
             fetch(0, F, k_of(next_slot, next_hv), kTile);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            *reinterpret_cast<uint4 *>(C + gtile(i, c0 + 8 * k)) = low[k];
+            *reinterpret_cast<uint4 *>(D + gtile(i, c0 + 8 * k)) = low[4 + k];
         }
         {
             float v[32];
@@ -519,6 +535,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
             gdn_mma(T0, desc_mn(A), kStepMN, desc_mn(E), kStepMN, idt, kGC / 16, 1);
             gdn_mma(T0, desc_k(G), kStepK, desc_mn(B), kStepMN, id, kGC / 16, 1);
             gdn_mma(T0, desc_mn(G), kStepMN, desc_mn(B), kStepMN, idt, kGC / 16, 1);
+            gdn_mma(T1, desc_k(C), kStepK, desc_mn(B), kStepMN, id, kGC / 16, 1);
+            gdn_mma(T0, desc_mn(C), kStepMN, desc_mn(E), kStepMN, idt, kGC / 16, 1);
+            gdn_mma(T0, desc_k(D), kStepK, desc_mn(B), kStepMN, id, kGC / 16, 1);
+            gdn_mma(T0, desc_mn(D), kStepMN, desc_mn(B), kStepMN, idt, kGC / 16, 1);
             tc::mma_commit(&s.done);
         }
         // dbeta and dg while they run
@@ -554,6 +574,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
         }
         all_done();
         if (tid == 0 && more && !*dead) {
+            fetch(0, C, p.dut + two_of(next_slot, next_hv), 2 * kTile);
             fetch(0, A, p.mt + two_of(next_slot, next_hv), kTile);
             fetch(0, G, p.mt + two_of(next_slot, next_hv) + kTile, kTile);
         }

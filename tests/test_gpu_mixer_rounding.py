@@ -32,5 +32,11 @@ def test_outputs_are_rounded_once(kda_lib, H, HV, K, V, decay):
     h0 = rnd(gen, len(lens), HV, K, V, std=0.3)
     kw = dict(initial_state=h0, cu_seqlens=cu, qk_l2norm=True)
     o, _ = kda.gated_delta_rule(*ins, **kw)
-    want, _ = om.gated_delta(*[f64(t) for t in ins], f64(h0), f64(cu).astype(int), l2=True)
+    ref = [f64(t) for t in ins]
+    want, _ = om.gated_delta(*ref, f64(h0), f64(cu).astype(int), l2=True)
     assert off(o, want) <= ONCE
+    do, dht = rnd(gen, 1, T, HV, V, dtype=torch.bfloat16), rnd(gen, len(lens), HV, K, V, std=0.3)
+    d = kda.gated_delta_backward(*ins, do, dht=dht, **kw)
+    want = om.gated_delta_grads(*ref, f64(do), f64(h0), f64(dht), f64(cu).astype(int), l2=True)
+    for name in ("dq", "dk", "dv", "dbeta"):
+        assert off(d[name], want[name]) <= ONCE, name
