@@ -287,6 +287,16 @@ __device__ __forceinline__ void store_vec(T *p, int n, const float (&v)[VEC]) {
 
 inline bool aligned_to(const void *p, size_t a) { return (uintptr_t)p % a == 0; }
 
+// A plain launch under a name that the profile knows; none for a grid without blocks.
+template <typename... A, typename... B>
+cudaError_t run(const char *name, void (*kernel)(A...), dim3 blocks, int threads, size_t smem, cudaStream_t st, B... args) {
+    if (blocks.x == 0) return cudaSuccess;
+    prof_begin(name, st);
+    kernel<<<blocks, threads, smem, st>>>(args...);
+    prof_end(st);
+    return cudaGetLastError();
+}
+
 // The packed-offset checks of every call, by the threads of one block: the work itself
 // clamps what it reads from the offsets, so bad ones cannot lead out of bounds.
 __device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, int32_t *status) {

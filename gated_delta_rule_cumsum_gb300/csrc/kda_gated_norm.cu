@@ -582,13 +582,6 @@ cudaError_t with_team(int n, bool vec, F &&f) {
                         Team<4, 2, 256>(), Team<4, 2, 512>(), Team<4, 2, 1024>(), Team<4, 4, 1024>());
 }
 
-template <typename... A, typename... B>
-cudaError_t run(const char *name, void (*kernel)(A...), dim3 grid, int threads, cudaStream_t st, B... args) {
-    prof_begin(name, st);
-    kernel<<<grid, threads, 0, st>>>(args...);
-    prof_end(st);
-    return cudaGetLastError();
-}
 bool all_at(size_t bytes, std::initializer_list<const void *> ps) {
     for (const void *q : ps)
         if (!aligned_to(q, bytes)) return false;
@@ -610,7 +603,7 @@ cudaError_t gated(const GatedNormArgs &a, bool bwd, cudaStream_t st) {
         return with_fwd_team<T>(a.group, vec, [&](auto t) {
             using U = decltype(t);
             return run("gated_fwd", gated_fwd_kernel<T, U::vec, U::nv, U::ts>, fwd_grid<T, U>(units),
-                       block_threads(U::ts), st, a);
+                       block_threads(U::ts), 0, st, a);
         });
     }
     const int64_t rows = gated_bwd_rows(a.rows, a.parts, a.shared);
@@ -620,10 +613,10 @@ cudaError_t gated(const GatedNormArgs &a, bool bwd, cudaStream_t st) {
         e = with_team<T>(a.group, vec, [&](auto t) {
             using U = decltype(t);
             return run("gated_bwd", gated_bwd_kernel<T, U::vec, U::nv, U::ts>,
-                       dim3((unsigned)(a.shared ? rows : rows * a.parts)), block_threads(U::ts), st, a);
+                       dim3((unsigned)(a.shared ? rows : rows * a.parts)), block_threads(U::ts), 0, st, a);
         });
     if (e == cudaSuccess)
-        e = run("part_sum", part_sum_kernel, dim3((unsigned)((n + 31) / 32)), 1024, st, (const float *)a.part, rows, n,
+        e = run("part_sum", part_sum_kernel, dim3((unsigned)((n + 31) / 32)), 1024, 0, st, (const float *)a.part, rows, n,
                 a.dw, a.dw, a.dw);
     return e;
 }
@@ -639,19 +632,19 @@ cudaError_t sandwich(const SandwichArgs &a, bool bwd, cudaStream_t st) {
             using U = decltype(t);
             return run("sandwich_fwd", a.z ? sandwich_fwd_kernel<T, U::vec, U::nv, U::ts, true>
                                            : sandwich_fwd_kernel<T, U::vec, U::nv, U::ts, false>,
-                       fwd_grid<T, U>(a.rows), block_threads(U::ts), st, a);
+                       fwd_grid<T, U>(a.rows), block_threads(U::ts), 0, st, a);
         });
     if (a.rows > 0 && bwd)
         e = with_team<T>(a.cols, vec, [&](auto t) {
             using U = decltype(t);
             return run("sandwich_bwd", a.z ? sandwich_bwd_kernel<T, U::vec, U::nv, U::ts, true>
                                            : sandwich_bwd_kernel<T, U::vec, U::nv, U::ts, false>,
-                       dim3((unsigned)sandwich_bwd_rows(a.rows)), block_threads(U::ts), st, a);
+                       dim3((unsigned)sandwich_bwd_rows(a.rows)), block_threads(U::ts), 0, st, a);
         });
     if (!bwd) return e;
     const int64_t blocks = sandwich_bwd_rows(a.rows);
     if (e == cudaSuccess)
-        e = run("part_sum", part_sum_kernel, dim3((unsigned)((a.cols + 31) / 32), a.drs ? 3 : 2), 1024, st,
+        e = run("part_sum", part_sum_kernel, dim3((unsigned)((a.cols + 31) / 32), a.drs ? 3 : 2), 1024, 0, st,
                 (const float *)a.part, blocks, a.cols, a.dw_post, a.dw_pre, a.drs);
     return e;
 }

@@ -939,15 +939,6 @@ cudaError_t prepare_kernels() {
     });
 }
 
-template <typename... A, typename... B>
-cudaError_t run(const char *name, void (*kernel)(A...), dim3 blocks, int threads, size_t smem, cudaStream_t st, B... args) {
-    if (blocks.x == 0) return cudaSuccess;
-    prof_begin(name, st);
-    kernel<<<blocks, threads, smem, st>>>(args...);
-    prof_end(st);
-    return cudaGetLastError();
-}
-
 // The offsets' check, norms and rows: what every path begins with.
 template <typename T>
 cudaError_t launch_rows(const GdnArgs &a, cudaStream_t st) {
@@ -962,9 +953,11 @@ cudaError_t launch_rows(const GdnArgs &a, cudaStream_t st) {
         e = run("gdn_norms", al ? gdn_norms_kernel<T, true> : gdn_norms_kernel<T, false>,
                 (((int64_t)a.B * a.T * a.H << log_lanes) + kThreads - 1) / kThreads, kThreads, 0, st, a, log_lanes);
     }
+    auto rows = gdn_rows_kernel<T, kGL / 32>;
+    if constexpr (sizeof(T) == 2)  // (fp32 has chunks of 32 rows only)
+        if (a.L != kGL) rows = gdn_rows_kernel<T, kGC / 32>;
     if (e == cudaSuccess)
-        e = run("gdn_rows", a.L == kGL ? gdn_rows_kernel<T, kGL / 32> : gdn_rows_kernel<T, kGC / 32>,
-                a.slots * ((a.HV + kRowHeads - 1) / kRowHeads), 32 * kRowHeads, 0, st, a);
+        e = run("gdn_rows", rows, a.slots * ((a.HV + kRowHeads - 1) / kRowHeads), 32 * kRowHeads, 0, st, a);
     return e;
 }
 

@@ -768,19 +768,6 @@ __global__ void __launch_bounds__(kOutThreads, 2) gdn_tc_out_kernel(GdnArgs p, i
     tmem_close(tm, 256);
 }
 
-bool rows16(const void *p, int64_t stride, int cols) {
-    return aligned_to(p, 16) && stride % 8 == 0 && cols % 8 == 0;
-}
-
-template <typename... A, typename... B>
-cudaError_t run(const char *name, void (*kernel)(A...), int64_t blocks, int threads, size_t smem, cudaStream_t st, B... args) {
-    if (blocks == 0) return cudaSuccess;
-    prof_begin(name, st);
-    kernel<<<(unsigned)blocks, threads, smem, st>>>(args...);
-    prof_end(st);
-    return cudaGetLastError();
-}
-
 cudaError_t prepare_kernels() {
     static DeviceOnce once;
     int dev;

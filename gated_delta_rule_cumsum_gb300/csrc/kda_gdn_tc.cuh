@@ -60,6 +60,9 @@ __device__ __forceinline__ void bf16x8(const uint4 &u, float (&v)[8]) {
     load_vec<__nv_bfloat16, 8, true>(reinterpret_cast<const __nv_bfloat16 *>(&u), 8, v);
 }
 
+// Whether rows can be copied 16 bytes at a time.
+inline bool rows16(const void *p, int64_t stride, int cols) { return aligned_to(p, 16) && stride % 8 == 0 && cols % 8 == 0; }
+
 // 128 rows of bf16 into a tile by TH threads; rows past nr and columns past nc (a multiple of 8)
 // are zeros.  Eight lanes take eight rows of one 16-byte column.  The copies are asynchronous
 // where the rows start on 16-byte boundaries.

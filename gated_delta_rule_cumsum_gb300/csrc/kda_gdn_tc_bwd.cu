@@ -641,17 +641,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) gdn_tc_grad_kernel(GdnArgs p,
     tmem_close(tm, 512);
 }
 
-bool rows16(const void *p, int64_t stride) { return aligned_to(p, 16) && stride % 8 == 0; }
-
-template <typename... A, typename... B>
-cudaError_t run(const char *name, void (*kernel)(A...), int64_t blocks, int threads, size_t smem, cudaStream_t st, B... args) {
-    if (blocks == 0) return cudaSuccess;
-    prof_begin(name, st);
-    kernel<<<(unsigned)blocks, threads, smem, st>>>(args...);
-    prof_end(st);
-    return cudaGetLastError();
-}
-
 cudaError_t prepare_kernels() {
     static DeviceOnce once;
     int dev;
@@ -674,7 +663,7 @@ static_assert(2 * (sizeof(BaseSmem) + 1024) <= 233472, "an SM's shared memory");
 cudaError_t launch_gdn_tc_bwd(const GdnArgs &a, cudaStream_t st) {
     cudaError_t e = prepare_kernels();
     if (e != cudaSuccess) return e;
-    const bool al = rows16(a.q, a.q_stride) && rows16(a.v, a.v_stride) && aligned_to(a.dout, 16);
+    const bool al = rows16(a.q, a.q_stride, a.K) && rows16(a.v, a.v_stride, a.V) && aligned_to(a.dout, 16);
     const int wide = (aligned_to(a.dv, 32) && a.V % 16 == 0 ? 1 : 0) |
                      (aligned_to(a.dq, 32) && aligned_to(a.dk, 32) && a.K % 16 == 0 ? 2 : 0);
     auto base = [&](const GdnArgs &x, int64_t units, cudaStream_t on) {
