@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gdn_tc_prep_kernel(GdnArgs p)
 // has an SM of its own the copies are two rounds ahead.
 // Bound by the chain: 8192 rows of 16 heads (64 blocks, 64 rounds) 130 us forward and 143 in reverse, 2 us a round, of
 // which the products take 0.6; 28 sequences of 32 heads (3584 blocks) 278 us.
-constexpr int kScanRows = 256, kScanThreads = kScanRows + 32, kAhead = 3;
+constexpr int kScanRows = 256, kScanThreads = kScanRows + 32;
 template <int BUFS>
 struct ScanSmem {
     uint8_t w[BUFS][2 * kTile], k[BUFS][kTile];
@@ -432,32 +432,15 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
                 ++k_due;
             }
         };
-        // what a later round of the reverse pass will read, into L2: its rounds have more to load (172 against
-        // 194 us at 8192 rows of 16 heads; the forward pass took 162 against 156)
-        auto ahead = [&](int n) {
-            if (!REV || BUFS > 1 || n >= nc) return;
-            const int64_t unit = slot_of(n) * p.HV + hv;
-            if (lane < 4) {
-                prefetch_l2(p.du0 + unit * kGC * kGD + wide_at(tile, 2 * lane, 0), kTile / 8);
-                prefetch_l2(p.b0 + unit * kGC * kGD + wide_at(tile, 2 * lane, 0), kTile / 8);
-            }
-            if (n % vt == tile) {
-                if (lane < 16) prefetch_l2(p.wt + unit * 2 * (int64_t)kTile + lane * (kTile / 8), kTile / 8);
-                if (lane >= 16 && lane < 24)
-                    prefetch_l2(p.kt + (slot_of(n) * p.H + h) * (int64_t)kTile + (lane - 16) * (kTile / 8), kTile / 8);
-            }
-        };
         for (int n = 0; n < BUFS; ++n) {
             next(true, n);
             next(false, n);
         }
-        for (int n = 1; n < kAhead; ++n) ahead(n);
         for (int n = 0; n < nc; ++n) {
             const int at = n % BUFS, turn = n / BUFS & 1;
             const uint8_t *w = s.w[at], *k = s.k[at];
             bool ok = lane != 0 || copies_or_die(p, REV ? &s.k_full[at] : &s.w_full[at], turn, dead);
             __syncwarp();
-            ahead(n + kAhead);
             bar_sync(1, kScanThreads);  // the state's tile is written
             tc::tc_fence_after();
             if (lane == 0 && ok) {

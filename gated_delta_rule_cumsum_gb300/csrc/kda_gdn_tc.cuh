@@ -117,9 +117,6 @@ __device__ __forceinline__ void decays16(const GdnRows &rd, int i, int quad, int
         for (int k = 0; k < 16; ++k) w[k] = 0.f;
     }
 }
-__device__ __forceinline__ void prefetch_l2(const void *from, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
-}
 // A unit's rows into shared memory, by all threads.
 __device__ __forceinline__ void load_rows_of(float *to, const GdnArgs &p, int64_t unit, int tid, int threads) {
     const float4 *from = reinterpret_cast<const float4 *>(p.rows + unit * kGdnRowArrays * kGC);
