@@ -326,6 +326,10 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         const bool live = unit < units;
         const int64_t row = !live ? 0 : p.shared ? (uint32_t)unit / (uint32_t)p.parts : unit;
         const int g0 = !live ? 0 : p.shared ? (int)((uint32_t)unit % (uint32_t)p.parts) * n : own;
+        // sigmoid(-|z|) for the second round: formed again in blocks of 1024 threads, whose 64 registers a thread
+        // would spill it (4096 x 16384: bf16 495 us kept and 332 formed again, fp32 870 and 668), but for fp32 with
+        // scalar accesses, where the exponential's registers spill in its place (2048 x 16382: 659 and 1073)
+        constexpr bool keep = TS < 1024 || (VEC == 1 && sizeof(T) == 4);
         P x, z, sg, d;
         widen(xr, x);
         widen(zr, z);
@@ -334,8 +338,8 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         uint64_t vv = 0, ev = 0;
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
-            sg.v[e] = small_of<T>(z.v[e]);
-            const uint64_t a = gate_from(z.v[e], sg.v[e], p.act);
+            if (keep) sg.v[e] = small_of<T>(z.v[e]);
+            const uint64_t a = keep ? gate_from(z.v[e], sg.v[e], p.act) : gate_of<T>(z.v[e], p.act);
             const uint64_t v = p.first ? mul2(x.v[e], a) : x.v[e];  // what is normalised
             uint64_t g = mul2(d.v[e], w.v[e]);                      // dL/d(rms(v))
             if (!p.first) g = mul2(g, a);
@@ -349,7 +353,8 @@ __global__ void __launch_bounds__(block_threads(TS), bwd_blocks(TS))
         const uint64_t r = both(rs), m = both(-(s[1] / n * rs * rs * rs));
 #pragma unroll
         for (int e = 0; e < P::N; ++e) {
-            const uint64_t a = gate_from(z.v[e], sg.v[e], p.act), da = dgate_from(z.v[e], sg.v[e], p.act);
+            const uint64_t sm = keep ? sg.v[e] : small_of<T>(z.v[e]);
+            const uint64_t a = gate_from(z.v[e], sm, p.act), da = dgate_from(z.v[e], sm, p.act);
             const uint64_t gw = mul2(d.v[e], w.v[e]), xv = x.v[e];
             if (p.first) {
                 const uint64_t v = mul2(xv, a), dt = fma2(v, m, mul2(r, gw));
