@@ -9,8 +9,9 @@
 // registers.  Teams are parts of a warp, a warp or a block, so that a thread has one to four
 // 16-byte vectors of each tensor; without 16-byte alignment (32 for the weights of bf16 inputs)
 // a thread's columns are dealt in turn.
-// Measured, bf16: gated 8192 x 4096 in one group 36 us (5.6 TB/s), 8192 x 16 groups of 128 21 us (4.8), its gradients 37 us and 6 for their sums (67%); sandwich 8192 x 4096 without a gate 48 us
-// (5.6 TB/s), 8192 x 2048 with one 32 us (5.2), its gradients 72 us and 10 (3.3 TB/s: the registers, which
+// Measured, bf16, inputs not in L2: gated 8192 x 4096 in one group 35 us (5.7 TB/s), 8192 x 16 groups of 128 21 us
+// (4.8), its gradients 39 us and 6 for their sums (4.3 TB/s: issue slots, 69% busy); sandwich 8192 x 4096 without a gate
+// 47 us (5.7 TB/s), 8192 x 2048 with one 32 us (5.2), its gradients 72 us and 10 (3.7 TB/s: the registers, which
 // leave 16 warps an SM).
 #include <initializer_list>
 
@@ -201,7 +202,8 @@ __host__ __device__ constexpr int block_teams(int ts) { return block_threads(ts)
 // bytes.  They stay and walk the rows, the next row's loads ahead.  Measured with the 16 columns that a
 // thread has of 8192 rows of 4096 in bf16: 768 threads an SM 52 us (sandwich) and 38 us (gated), 512
 // (no spills) 60 and 42; 8 columns and 1024 threads 62 and 45; 32 columns and 512 threads 50 and 37, but with a
-// gate 45 us where 16 columns take 35 (sandwich, 2048 columns).
+// gate 45 us where 16 columns take 35 (sandwich, 2048 columns).  Blocks of 512 threads (groups of 4097 to 8192
+// columns in bf16) do not add up to 768: there is one of them on an SM.
 __host__ __device__ constexpr int fwd_blocks(int ts, int count, int size) {
     const int threads = count <= 8 && count * size <= 16 ? 1024 : count * size <= 32 ? 768 : 512;
     return threads / block_threads(ts) > 0 ? threads / block_threads(ts) : 1;
@@ -558,8 +560,8 @@ template <typename F, typename Head, typename... Tail>
 cudaError_t first_of(int n, F &&f, Head head, Tail... tail) {
     return Head::vec * Head::nv * Head::ts >= n ? f(head) : first_of(n, f, tail...);
 }
-// Forward: 16 columns per thread past 64 (see fwd_blocks; groups of 128 of 8192 x 2048 with eight each: 25 us for
-// 23).
+// Forward: 16 columns per thread past 64 (see fwd_blocks; groups of 128 of 8192 x 2048, inputs in L2: 18.6 us so, 20.3
+// with eight each).
 template <typename T, typename F>
 cudaError_t with_fwd_team(int n, bool vec, F &&f) {
     if (!vec)

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) gdn_norms_kernel(GdnArgs p, int log_
 // are taken as this one, so that the differences of the rows behind it keep their digits.
 constexpr float kReset = -8192.f;
 // The rows' decays: a block per chunk and 16 value heads, whose inputs come in whole sectors; then a
-// warp per head, L / 32 consecutive rows per lane.  8192 rows of 16 heads: 10 us, the launch and one
+// warp per head, L / 32 consecutive rows per lane.  8192 rows of 16 heads: 7 us, the launch and one
 // round of loads.
 constexpr int kRowHeads = 16;
 template <typename T, int PER>

@@ -16,7 +16,7 @@ using bf16 = __nv_bfloat16;
 // tcgen05.mma has 64 rows at least, of two tf32 parts each (2^-22), and the two halves of 64 rows with
 // tcgen05 products.  W and U0 take M from tensor memory with its columns scaled, so that K and V enter as
 // they were loaded.
-// 8192 rows of 16 heads (1024 units, two blocks an SM): 84 us; 4 x 4096 rows of 32 heads 293 us.  A unit is a chain of
+// 8192 rows of 16 heads (1024 units, two blocks an SM): 83 us; 4 x 4096 rows of 32 heads 293 us.  A unit is a chain of
 // some fifteen hand-overs; issue slots are 45% busy, HBM 29%.  Substitution in blocks of 8 in place of 16
 // changed nothing.
 constexpr int kPrepThreads = 256;
@@ -369,8 +369,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gdn_tc_prep_kernel(GdnArgs p)
 // are fetched again as soon as the product that reads them is through, which leaves them the rest of the
 // round; with one buffer each (BUFS), two blocks share an SM and fill each other's waits.  Where every block
 // has an SM of its own the copies are two rounds ahead.
-// Bound by the chain: 8192 rows of 16 heads (64 blocks, 64 rounds) 130 us forward and 143 in reverse, 2 us a round, of
-// which the products take 0.6; 28 sequences of 32 heads (3584 blocks) 278 us.
+// Bound by the chain: 8192 rows of 16 heads (64 blocks, 64 rounds) 128 us forward and 139 in reverse, 2 us a round, of
+// which the products take 0.6; 28 sequences of 32 heads (3584 blocks) 288 us, 4 x 4096 rows of 32 heads 213 and 273.
+// Copies into L2 ahead of a round's own, in the reverse pass with one buffer: 312 us for those 273.
 constexpr int kScanRows = 256, kScanThreads = kScanRows + 32;
 template <int BUFS>
 struct ScanSmem {
@@ -615,10 +616,10 @@ __global__ void __launch_bounds__(kScanThreads, 3 - BUFS) gdn_tc_scan_kernel(Gdn
 // O = diag(rq) (diag(c) Q S + P U) for a chunk, one block each, two on an SM.  P and U are two bf16
 // parts: where keys are alike, U's rows nearly cancel in the sum (one part each left o off by 3% of
 // its largest value for keys that are all but the same); so is the state (one part left o off by half of what
-// its own rounding does, and the kernel at 132 of its 155 us).  P is a left operand in tensor memory, over the gram it is
+// its own rounding does, and the kernel at 132 of its 151 us).  P is a left operand in tensor memory, over the gram it is
 // made of, and its products are added to the state's.  Of the seven tiles three have room at a time: each is fetched
-// as soon as the product with the one before it is through.  8192 rows of 16 heads: 54 us for 230 MB, 4.3 TB/s; 4 x 4096
-// rows of 32 heads 155 us.
+// as soon as the product with the one before it is through.  8192 rows of 16 heads: 51 us for 230 MB, 4.5 TB/s; 4 x 4096
+// rows of 32 heads 151 us.
 constexpr int kOutThreads = 256;
 struct OutSmem {
     uint8_t q[kTile], k[kTile], s[kTile];  // Q, then U's low part; K, then the state's low part; its high part, then U's
@@ -865,9 +866,10 @@ GdnSideHold::~GdnSideHold() {
 // free, at `unit_ns` of the whole card per unit; a pass's round takes `round_ns`.  Only where there are
 // `least` units (launches and joins cost some 20 us) and the pass has at most two thirds of the SMs, and not
 // inside a capture: a graph would hold the library's stream until it ends.  Measured, a training pass (and a
-// forward) in one part and in two, B = 1, K = V = 128: 8192 rows, 16 heads 695 and 598 us (290, 277); 8 heads 519
-// and 452 (229, 213); 4 heads 403 and 399 (195, 201); 32 heads 1063 and 1151; 2048 rows, 16 heads 225 and 238 (102,
-// 113).
+// forward) in one part and in two, B = 1, K = V = 128: 8192 rows, 24 heads 924 and 867 us (357, 330); 16 heads 704 and
+// 625 (286, 260 to 286: which kernel finds the SMs first is open); 8 heads 519 and 467 (224, 220); 4 heads 399 and 390
+// (181, 195: one part); 32768 rows of 4 heads 1458 and 1311 (661, 612); refused: 32 heads 1091 and 1220 (410, 427),
+// 2048 rows of 16 heads 212 and 245 (89, 110).
 int gdn_cut(const GdnArgs &a, double unit_ns, double round_ns, int64_t least, cudaStream_t st) {
     const int nc = (a.T + a.L - 1) / a.L;
     const int64_t scans = scan_blocks(a);

@@ -172,7 +172,7 @@ class GdnSideHold {
 };
 int gdn_cut(const GdnArgs &a, double unit_ns, double round_ns, int64_t least, cudaStream_t st);
 // Measured: the whole card's time per unit of the prep and of the gradients, and a pass's round.
-constexpr double kPrepNs = 85, kGradNs = 205, kRoundNs = 2200;
+constexpr double kPrepNs = 82, kGradNs = 215, kRoundNs = 2150;
 cudaError_t launch_gdn_tc_rscan(const GdnArgs &a, cudaStream_t st);
 cudaError_t launch_gdn_tc_bwd(const GdnArgs &a, cudaStream_t st);
 

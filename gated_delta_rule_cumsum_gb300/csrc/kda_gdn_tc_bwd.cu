@@ -12,7 +12,7 @@ using bf16 = __nv_bfloat16;
 // ------------------------------------------------------------------ what the outputs give
 // dU0 = P^T dO and B0 = Q^T diag(rq c) dO, for the reverse pass, in fp32.  P and the scaled dO are two
 // bf16 parts; P's are multiplied one after the other from the same tile, so that two blocks fit
-// an SM.  8192 rows of 16 heads: 60 us for 230 MB, 3.8 TB/s.
+// an SM.  8192 rows of 16 heads: 57 us for 230 MB, 4.0 TB/s.
 constexpr int kBaseThreads = 256;
 struct BaseSmem {
     uint8_t q[kTile], k[kTile], d[kTile];  // Q; K, then P's parts and the scaled dO's low part; dO
@@ -150,10 +150,10 @@ __global__ void __launch_bounds__(kBaseThreads, 2) gdn_tc_base_kernel(GdnArgs p)
 // projection.
 // Each block takes every n-th unit; the next unit's tiles are fetched as soon as this one's leave room
 // (224 KB are a quarter of a unit's time), which moves the tiles' parts around: see the loop's end.
-// 8192 rows of 16 heads: 225 us, 33 us a unit, of which its products take 7.  One unit an SM is a chain of
+// 8192 rows of 16 heads: 219 us, 32 us a unit, of which its products take 7.  One unit an SM is a chain of
 // four rounds of products and what the threads do between them; HBM is 34% busy, and no shared memory is left
 // for a second unit.  X and Y with one part each (208 us) left dq and dk off by 2.5e-3 from the rounded ones; their
-// low parts by bulk copies, which want a fence between the threads' writes and the copy, 240 us.
+// low parts by bulk copies, which want a fence between the threads' writes and the copy, some 235.
 constexpr int kGradThreads = 512;
 struct GradSmem {
     uint8_t t[7][kTile];
