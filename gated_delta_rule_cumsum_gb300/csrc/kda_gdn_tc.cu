@@ -844,7 +844,7 @@ GdnSideHold::GdnSideHold(cudaStream_t st) {
             }
             if (!idle && (!s.last || cudaEventQuery(s.last) == cudaSuccess)) idle = &s;
         }
-        cudaGetLastError();  // (a query's "not ready")
+        if (cudaPeekAtLastError() == cudaErrorNotReady) cudaGetLastError();  // (the query's; nobody else's error)
         if (idle && !idle->stream) error = make_side(*idle);
         if (idle && error == cudaSuccess) {
             idle->taken = true;
