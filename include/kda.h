@@ -638,6 +638,7 @@ size_t kda_add_rmsnorm_bwd_workspace_size(const kda_norm_shape *shape);
  *     S_t = 2^{g_t} S_{t-1} + beta_t k_t (v_t - (2^{g_t} S_{t-1})^T k_t)^T,   o_t = scale S_t^T q_t.
  * Every exponent is a difference of cumulative decays taken before the exponential, so that
  * no range of g <= 0 is refused in either direction; g = -inf drops the state before the row.
+ * The conventions are the recurrent block's.
  */
 
 /* flags of kda_gdn_shape */
@@ -704,7 +705,10 @@ kda_status kda_gdn_step(const void *q, const void *k, const void *v, const float
                         const kda_gdn_shape *shape, void *o, int32_t *dev_status, kda_stream_t stream);
 
 /* ------------------------------------------------------------------------------
- * The norms around a gated block.  rms(x) = x / sqrt(mean(x^2) + eps).
+ * The norms around a gated block.  rms(x) = x / sqrt(mean(x^2) + eps).  The conventions are the
+ * recurrent block's: outputs overlap neither inputs nor each other.  Values that are not finite reach
+ * their row (in the gated norm their group of it) and, in the gradients, the weights' gradients
+ * of its columns.
  */
 typedef enum {
     KDA_GATE_SIGMOID = 0,       /* act(z) = sigmoid(z)                                  */
