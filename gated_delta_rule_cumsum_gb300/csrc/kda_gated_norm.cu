@@ -162,7 +162,7 @@ __device__ __forceinline__ float gate_exp(float x) {
     else
         return expf(x);
 }
-// The activated gate.
+// The activated gate.  (A sigmoid below 2^-126, z < -87.3, comes out as 0.)
 template <typename T>
 __device__ __forceinline__ uint64_t gate_of(uint64_t z, int act) {
     float a, b;
